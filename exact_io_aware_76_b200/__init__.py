@@ -4,13 +4,13 @@ Every step of the computation runs in the library's CUDA kernels; this module on
 (PyTorch tensors -> device pointers, sizes and a CUDA stream) and turns status codes into exceptions. There is
 no fallback: if the library is missing or fails to load, every call raises.
 
-    fwd(q, k, v, causal=False, scale=None, window=(-1, -1)) -> (out, lse)
-    bwd(q, k, v, out, lse, dout, causal=False, scale=None, window=(-1, -1)) -> (dq, dk, dv)
+    fwd(q, k, v, causal=False, scale=None, window=(-1, -1), sinks=0) -> (out, lse)
+    bwd(q, k, v, out, lse, dout, causal=False, scale=None, window=(-1, -1), sinks=0) -> (dq, dk, dv)
 
 Layouts follow the C header (include/fa.h): q/out/dout [B, Sq, H, D], k/v [B, Sk, Hkv, D] (Hkv divides H:
 grouped or multi-query K/V heads), fp16 or bf16, contiguous, on one CUDA device; lse is fp32 [B, H, Sq].
 ``scale=None`` means 1/sqrt(D); ``window=(left, right)`` limits each query to keys within left before and
-right after its aligned key (-1 = unbounded side).
+right after its aligned key (-1 = unbounded side); the first ``sinks`` keys stay visible left of the window.
 
 Every operand (inputs and caller-passed outputs alike) is checked against these shapes, dtypes and the
 device of ``q`` before anything is launched; a mismatch raises ``ValueError`` or ``TypeError``. Each call
@@ -26,8 +26,9 @@ FA_F16, FA_BF16 = 0, 1
 FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", -1: "FA_ERR_INVALID", -2: "FA_ERR_UNSUPPORTED", -3: "FA_ERR_CUDA",
                 -4: "FA_ERR_TIMEOUT", -5: "FA_ERR_WORKSPACE"}
-EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_dropout", "fa_bwd_dropout", "fa_bwd", "fa_bwd_ex",
-           "fa_bwd_stage", "fa_bwd_noalloc", "fa_bwd_workspace_size", "fa_status_string", "fa_device_status")
+EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_dropout", "fa_fwd_sink", "fa_bwd_dropout", "fa_bwd",
+           "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace_size", "fa_bwd_stage", "fa_bwd_noalloc",
+           "fa_bwd_workspace_size", "fa_status_string", "fa_device_status")
 
 _lib = None
 
@@ -68,6 +69,12 @@ def lib():
                                  vp, sz, vp]
     L.fa_bwd_ex.restype = i
     L.fa_bwd_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, i, vp, sz, vp]
+    L.fa_fwd_sink.restype = i
+    L.fa_fwd_sink.argtypes = [vp] * 5 + [i] * 10 + [f, i, vp]
+    L.fa_bwd_sink.restype = i
+    L.fa_bwd_sink.argtypes = [vp] * 9 + [i] * 10 + [f, i, vp, sz, vp]
+    L.fa_bwd_sink_workspace_size.restype = sz
+    L.fa_bwd_sink_workspace_size.argtypes = [i] * 10
     L.fa_bwd_workspace_size.restype = sz
     L.fa_bwd_workspace_size.argtypes = [i, i, i, i]
     L.fa_status_string.restype = ctypes.c_char_p
@@ -147,6 +154,13 @@ def check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B,
             raise ValueError("workspace must hold at least %d bytes" % ws_bytes)
 
 
+def check_sinks(sinks, dropout_p):
+    if int(sinks) != sinks or not 0 <= sinks < 2 ** 31:
+        raise ValueError("sinks must be a number of keys (a 32-bit integer >= 0), got %r" % (sinks,))
+    if sinks and dropout_p:
+        raise ValueError("sinks and dropout do not go together")
+
+
 def _stream(stream, dev):
     import torch
 
@@ -164,29 +178,33 @@ def _device(dev):
 
 # ------------------------------------------------------------------------------------------ entry points
 def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, window=(-1, -1), dropout_p=0.0, seed=0,
-        offset=0):
+        offset=0, sinks=0):
     """Forward attention. Returns (out [B,Sq,H,D] in q's dtype, lse fp32 [B,H,Sq]).
 
-    ``dropout_p`` > 0 drops attention probabilities with the Philox mask of ``fa_fwd_dropout`` (include/fa.h),
+    ``sinks`` > 0 keeps the first ``sinks`` keys visible left of the window (``fa_fwd_sink``; not together with
+    dropout). ``dropout_p`` > 0 drops attention probabilities with the Philox mask of ``fa_fwd_dropout`` (include/fa.h),
     keyed by ``seed`` (64-bit) and ``offset`` (32-bit); the backward must get the same three values."""
     import torch
 
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
+    check_sinks(sinks, dropout_p)
     with _device(dev):
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
-        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
-                int(bool(causal)), int(window[0]), int(window[1]), float(0.0 if scale is None else scale),
-                _dtype_code(q))
+        shape = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
+                 int(bool(causal)), int(window[0]), int(window[1]))
+        sc = (float(0.0 if scale is None else scale), _dtype_code(q))
         if dropout_p:
-            rc = lib().fa_fwd_dropout(*args, float(dropout_p), int(seed), int(offset), _stream(stream, dev))
+            rc = lib().fa_fwd_dropout(*shape, *sc, float(dropout_p), int(seed), int(offset), _stream(stream, dev))
+        elif sinks:
+            rc = lib().fa_fwd_sink(*shape, int(sinks), *sc, _stream(stream, dev))
         else:
-            rc = lib().fa_fwd_ex(*args, _stream(stream, dev))
+            rc = lib().fa_fwd_ex(*shape, *sc, _stream(stream, dev))
     if rc != FA_OK:
-        raise FAError(rc, "fa_fwd_dropout" if dropout_p else "fa_fwd_ex")
+        raise FAError(rc, "fa_fwd_dropout" if dropout_p else "fa_fwd_sink" if sinks else "fa_fwd_ex")
     return out, lse
 
 
@@ -216,8 +234,14 @@ def workspace_size(B, Sq, H, D):
     return int(lib().fa_bwd_workspace_size(B, Sq, H, D))
 
 
+def sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks):
+    """Bytes of workspace the backward with ``sinks`` needs."""
+    return int(lib().fa_bwd_sink_workspace_size(B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]),
+                                                int(window[1]), int(sinks)))
+
+
 def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None,
-        stage=-1, window=(-1, -1), dropout_p=0.0, seed=0, offset=0):
+        stage=-1, window=(-1, -1), dropout_p=0.0, seed=0, offset=0, sinks=0):
     """Backward attention (P recomputed from lse). Returns (dq, dk, dv) in q's dtype.
 
     ``stage`` selects one of the three launches (0 preprocess, 1 main, 2 dQ conversion; -1 all), see
@@ -225,13 +249,17 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
     import torch
 
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
-    if stage != -1 and (dropout_p or Hkv != H or tuple(window) != (-1, -1)):
+    check_sinks(sinks, dropout_p)
+    if stage != -1 and (dropout_p or Hkv != H or tuple(window) != (-1, -1) or sinks):
         raise ValueError("single backward stages are available for plain attention only")
     with _device(dev):
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
-        ws_bytes = workspace_size(B, Sq, H, D)
+        if sinks:
+            ws_bytes = sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks)
+        else:
+            ws_bytes = workspace_size(B, Sq, H, D)
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Sq, H, D, dev)
         if workspace is None:
             workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
@@ -242,6 +270,9 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
         if dropout_p:
             rc = lib().fa_bwd_dropout(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
                                       sc, _dtype_code(q), float(dropout_p), int(seed), int(offset), *ws_args)
+        elif sinks:
+            rc = lib().fa_bwd_sink(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
+                                   int(sinks), sc, _dtype_code(q), *ws_args)
         elif stage == -1:
             rc = lib().fa_bwd_ex(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]), sc,
                                  _dtype_code(q), *ws_args)
@@ -249,7 +280,7 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
             rc = lib().fa_bwd_stage(int(stage), *ptrs, B, Sq, Sk, H, D, int(bool(causal)), sc, _dtype_code(q),
                                     *ws_args)
     if rc != FA_OK:
-        raise FAError(rc, "fa_bwd")
+        raise FAError(rc, "fa_bwd_sink" if sinks else "fa_bwd")
     return dq, dk, dv
 
 

@@ -149,12 +149,12 @@ int check_common(int B, int Sq, int Sk, int H, int D, float scale, int dtype) {
   return FA_OK;
 }
 
-template <int D, bool BF16, bool CAUSAL, bool FP8 = false, bool DROP = false>
+template <int D, bool BF16, bool CAUSAL, bool FP8 = false, bool DROP = false, bool SINK = false>
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FwdParams& p, int dev,
                cudaStream_t stream) {
   using L = FwdSmem<D, FP8>;
   static bool attr_done[kMaxDevices] = {};
-  auto kern = fa::fa_fwd_kernel<D, BF16, CAUSAL, FP8, DROP>;
+  auto kern = fa::fa_fwd_kernel<D, BF16, CAUSAL, FP8, DROP, SINK>;
   int rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done);
   if (rc) return rc;
   const unsigned grid = (unsigned)(p.n_qblk * p.B * p.H);
@@ -165,6 +165,9 @@ int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
 template <int D, bool BF16>
 int dispatch_fwd_causal(bool causal, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const FwdParams& p, int dev, cudaStream_t s) {
+  if (p.sinks > 0)
+    return causal ? launch_fwd<D, BF16, true, false, false, true>(tq, tk, tv, p, dev, s)
+                  : launch_fwd<D, BF16, false, false, false, true>(tq, tk, tv, p, dev, s);
   if (p.drop_t != 0)
     return causal ? launch_fwd<D, BF16, true, false, true>(tq, tk, tv, p, dev, s)
                   : launch_fwd<D, BF16, false, false, true>(tq, tk, tv, p, dev, s);
@@ -178,6 +181,48 @@ struct BwdLayout {
   size_t dq_acc, dvec, lse2, total;
   int sq_pad;
 };
+
+// Sinks of a window bounded on the left: `sinks` first keys stay visible. Where the left bound hides no key, or every
+// key is a sink, the bound is dropped and the plain path runs (sinks = 0).
+struct SinkPlan {
+  int window_left, sinks;
+  int tiles, pieces;  // backward: key tiles that hold sinks, CTAs per such tile
+  size_t part_bytes;  // backward: fp32 partial sums of the pieces
+};
+constexpr int kSmCount = 148;  // a fixed number, so that workspace sizes need no device
+
+SinkPlan sink_plan(int B, int Sq, int Sk, int H, int Hkv, int D, int causal, int window_left, int window_right,
+                   int sinks) {
+  SinkPlan s{window_left, sinks, 0, 1, 0};
+  if (sinks == 0 || window_left < 0) {
+    s.sinks = 0;
+    return s;
+  }
+  if (window_left >= Sk - 1 || sinks >= Sk) {
+    s.window_left = -1;
+    s.sinks = 0;
+    return s;
+  }
+  // A sink tile takes group * ceil(Sq / 128) iterations (query tiles), another one about group * (window / 128 + 2).
+  // A CTA of the grid's front may run a quarter of an SM's fair share of all iterations without becoming the tail,
+  // and needs no less than a window tile's; longer sink tiles are cut into pieces of that length.
+  s.tiles = (sinks + 127) / 128;
+  const long long group = H / Hkv, q_tiles = (Sq + 127) / 128, k_tiles = (Sk + 127) / 128;
+  long long span = q_tiles;  // query tiles that see a window tile
+  const int right = causal ? 0 : window_right;
+  if (right >= 0) {
+    const long long w = ((long long)window_left + right + 127) / 128 + 2;
+    if (w < span) span = w;
+  }
+  const long long it_sink = group * q_tiles, it_win = group * span;
+  const long long fair = (long long)B * Hkv * (s.tiles * it_sink + (k_tiles - s.tiles) * it_win) / kSmCount;
+  long long len = fair / 4 > it_win ? fair / 4 : it_win;
+  if (len < 1) len = 1;
+  long long pieces = (it_sink + len - 1) / len;
+  s.pieces = (int)(pieces > 64 ? 64 : pieces);
+  if (s.pieces > 1) s.part_bytes = (size_t)B * Hkv * s.tiles * s.pieces * 2 * 128 * D * sizeof(float);
+  return s;
+}
 
 // Workspace: fp32 dQ accumulator (B*H*Sq_pad*D floats: [B,H,Sq_pad,64] for head dim 64, [B,H,Sq_pad/4,128,4]
 // for head dim 128), then D_i [B,H,Sq_pad], then LSE_i*log2(e) [B,H,Sq_pad].
@@ -202,7 +247,7 @@ int grid_for(long long work, int per_block, int dev) {
 // stage -1: all three launches; 0: preprocess; 1: main; 2: dQ conversion. Head dim 128 runs the 128-query-tile
 // main kernel (fa_bwd128.cuh) and the matching dQ conversion (query-quad accumulator layout); head dim 64 the
 // kernel of fa_bwd.cuh.
-template <int D, bool BF16, bool CAUSAL, bool DROP = false>
+template <int D, bool BF16, bool CAUSAL, bool DROP = false, bool SINK = false>
 int launch_bwd(int stage, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                const CUtensorMap& tdo, const BwdParams& p, int dev, cudaStream_t stream) {
   static bool attr_done[kMaxDevices] = {};
@@ -213,19 +258,26 @@ int launch_bwd(int stage, const CUtensorMap& tq, const CUtensorMap& tk, const CU
   }
   if (stage < 0 || stage == 1) {
     if constexpr (D == 128) {
-      const unsigned grid = (unsigned)(p.n_grp * p.B * p.Hkv);
-      auto kern = fa::fa_bwd_main128_kernel<BF16, CAUSAL, DROP>;
+      const unsigned grid = (unsigned)((p.n_grp + p.sink_tiles * (p.sink_pieces - 1)) * p.B * p.Hkv);
+      auto kern = fa::fa_bwd_main128_kernel<BF16, CAUSAL, DROP, SINK>;
       int rc = ensure_smem_attr(kern, Bwd128Smem::kAlloc, dev, attr_done);
       if (rc) return rc;
       kern<<<grid, Bwd128Smem::kThreads, Bwd128Smem::kAlloc, stream>>>(tq, tk, tv, tdo, p);
     } else {
-      const unsigned grid = (unsigned)(p.n_kblk * p.B * p.Hkv);
-      auto kern = fa::fa_bwd_main_kernel<D, BF16, CAUSAL, DROP>;
+      const unsigned grid = (unsigned)((p.n_kblk + p.sink_tiles * (p.sink_pieces - 1)) * p.B * p.Hkv);
+      auto kern = fa::fa_bwd_main_kernel<D, BF16, CAUSAL, DROP, SINK>;
       int rc = ensure_smem_attr(kern, BwdSmem<D>::kAlloc, dev, attr_done);
       if (rc) return rc;
       kern<<<grid, BwdSmem<D>::kThreads, BwdSmem<D>::kAlloc, stream>>>(tq, tk, tv, tdo, p);
     }
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if constexpr (SINK) {
+      if (p.sink_pieces > 1) {
+        const long long n = (long long)p.B * p.Hkv * p.sink_tiles * 2 * 128 * (D / 4);
+        fa::fa_bwd_sink_sum_kernel<D, BF16><<<grid_for(n, 256, dev), 256, 0, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+      }
+    }
   }
   if (stage < 0 || stage == 2) {
     if constexpr (D == 128) {
@@ -243,6 +295,9 @@ int launch_bwd(int stage, const CUtensorMap& tq, const CUtensorMap& tk, const CU
 template <int D, bool BF16>
 int dispatch_bwd_causal(int stage, bool causal, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const CUtensorMap& tdo, const BwdParams& p, int dev, cudaStream_t s) {
+  if (p.sinks > 0)
+    return causal ? launch_bwd<D, BF16, true, false, true>(stage, tq, tk, tv, tdo, p, dev, s)
+                  : launch_bwd<D, BF16, false, false, true>(stage, tq, tk, tv, tdo, p, dev, s);
   if (p.drop_t != 0)
     return causal ? launch_bwd<D, BF16, true, true>(stage, tq, tk, tv, tdo, p, dev, s)
                   : launch_bwd<D, BF16, false, true>(stage, tq, tk, tv, tdo, p, dev, s);
@@ -289,10 +344,10 @@ int dropout_threshold(float p) {
 }  // namespace
 
 static int fwd_impl(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Sq, int Sk, int H,
-                    int Hkv, int D, int causal, int window_left, int window_right, float scale, int dtype,
+                    int Hkv, int D, int causal, int window_left, int window_right, int sinks, float scale, int dtype,
                     float dropout_p, uint64_t seed, uint32_t offset, cudaStream_t stream) {
   const int drop_t = dropout_threshold(dropout_p);
-  if (drop_t < 0) return FA_ERR_INVALID;
+  if (drop_t < 0 || sinks < 0) return FA_ERR_INVALID;
   if (!q || !k || !v || !out || !lse) return FA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse)) return FA_ERR_INVALID;
   if (Hkv < 1 || H < 1 || H % Hkv != 0) return FA_ERR_INVALID;
@@ -301,6 +356,7 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   int dev = 0;
   if ((rc = current_device(&dev))) return rc;
   if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  const SinkPlan sp = sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks);
 
   CUtensorMap tq, tk, tv;
   if ((rc = make_bshd_map(&tq, q, B, Sq, H, D, dtype, 128))) return rc;
@@ -313,8 +369,9 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.win_left = window_left < 0 ? -1 : window_left;
+  p.win_left = sp.window_left < 0 ? -1 : sp.window_left;
   p.win_right = window_right < 0 ? -1 : window_right;
+  p.sinks = sp.sinks;
   p.Sq = Sq;
   p.Sk = Sk;
   p.n_qblk = (Sq + 255) / 256;
@@ -340,14 +397,21 @@ extern "C" {
 int fa_fwd_ex(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Sq, int Sk, int H,
               int Hkv, int D, int causal, int window_left, int window_right, float scale, int dtype,
               cudaStream_t stream) {
-  return fwd_impl(q, k, v, out, lse, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, scale, dtype, 0.f, 0,
-                  0, stream);
+  return fwd_impl(q, k, v, out, lse, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, 0, scale, dtype, 0.f,
+                  0, 0, stream);
+}
+
+int fa_fwd_sink(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Sq, int Sk, int H,
+                int Hkv, int D, int causal, int window_left, int window_right, int sinks, float scale, int dtype,
+                cudaStream_t stream) {
+  return fwd_impl(q, k, v, out, lse, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks, scale, dtype,
+                  0.f, 0, 0, stream);
 }
 
 int fa_fwd_dropout(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Sq, int Sk, int H,
                    int Hkv, int D, int causal, int window_left, int window_right, float scale, int dtype,
                    float dropout_p, uint64_t seed, uint32_t offset, cudaStream_t stream) {
-  return fwd_impl(q, k, v, out, lse, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, scale, dtype,
+  return fwd_impl(q, k, v, out, lse, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, 0, scale, dtype,
                   dropout_p, seed, offset, stream);
 }
 
@@ -379,6 +443,7 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* out, float* ls
   p.group = H / Hkv;
   p.win_left = window_left < 0 ? -1 : window_left;
   p.win_right = window_right < 0 ? -1 : window_right;
+  p.sinks = 0;
   p.Sq = Sq;
   p.Sk = Sk;
   p.n_qblk = (Sq + 255) / 256;
@@ -405,13 +470,21 @@ size_t fa_bwd_workspace_size(int B, int Sq, int H, int D) {
   return bwd_layout(B, Sq, H, D).total;
 }
 
+size_t fa_bwd_sink_workspace_size(int B, int Sq, int Sk, int H, int Hkv, int D, int causal, int window_left,
+                                  int window_right, int sinks) {
+  if (Hkv < 1 || H < 1 || H % Hkv != 0 || sinks < 0) return 0;
+  if (check_common(B, Sq, Sk, H, D, 1.f, FA_F16) != FA_OK) return 0;
+  return bwd_layout(B, Sq, H, D).total +
+         sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks).part_bytes;
+}
+
 static int bwd_impl(int stage, const void* q, const void* k, const void* v, const void* out, const float* lse,
                     const void* dout, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int Hkv, int D,
-                    int causal, int window_left, int window_right, float scale, int dtype, float dropout_p,
+                    int causal, int window_left, int window_right, int sinks, float scale, int dtype, float dropout_p,
                     uint64_t seed, uint32_t offset, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (stage < -1 || stage > 2) return FA_ERR_INVALID;
   const int drop_t = dropout_threshold(dropout_p);
-  if (drop_t < 0) return FA_ERR_INVALID;
+  if (drop_t < 0 || sinks < 0) return FA_ERR_INVALID;
   if (Hkv < 1 || H < 1 || H % Hkv != 0) return FA_ERR_INVALID;
   const void* ptrs[9] = {q, k, v, out, lse, dout, dq, dk, dv};
   for (const void* ptr : ptrs)
@@ -419,7 +492,9 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
   int rc = check_common(B, Sq, Sk, H, D, scale, dtype);
   if (rc) return rc;
   const BwdLayout lay = bwd_layout(B, Sq, H, D);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < lay.total)
+  const SinkPlan sp = sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < lay.total + sp.part_bytes)
     return FA_ERR_WORKSPACE;
   int dev = 0;
   if ((rc = current_device(&dev))) return rc;
@@ -446,8 +521,12 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.win_left = window_left < 0 ? -1 : window_left;
+  p.win_left = sp.window_left < 0 ? -1 : sp.window_left;
   p.win_right = window_right < 0 ? -1 : window_right;
+  p.sinks = sp.sinks;
+  p.sink_tiles = sp.tiles;
+  p.sink_pieces = sp.pieces;
+  p.sink_part = reinterpret_cast<float*>(ws + lay.total);
   p.Sq = Sq;
   p.Sk = Sk;
   p.Sq_pad = lay.sq_pad;
@@ -457,7 +536,7 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
   // carry equal work, so a partly empty last wave idles SMs (measured: 3.5 waves of 4-tile CTAs were 5.8% slower
   // than one tile per CTA, 6.9 waves of 8-tile CTAs 1.7% faster). One tile per CTA otherwise.
   p.units = 1;
-  if (D == 128)
+  if (D == 128 && p.sinks == 0)
     for (int u : {8, 4, 2}) {
       const long long ctas = (long long)B * Hkv * ((p.n_kblk + u - 1) / u), sms = g_dev[dev].sm_count;
       const long long waves = (ctas + sms - 1) / sms;
@@ -487,7 +566,7 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
 int fa_bwd_stage(int stage, const void* q, const void* k, const void* v, const void* out, const float* lse,
                  const void* dout, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int D, int causal,
                  float scale, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  return bwd_impl(stage, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, H, D, causal, -1, -1, scale, dtype,
+  return bwd_impl(stage, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, H, D, causal, -1, -1, 0, scale, dtype,
                   0.f, 0, 0, workspace, workspace_bytes, stream);
 }
 
@@ -496,7 +575,15 @@ int fa_bwd_ex(const void* q, const void* k, const void* v, const void* out, cons
               int window_right, float scale, int dtype, void* workspace, size_t workspace_bytes,
               cudaStream_t stream) {
   return bwd_impl(-1, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right,
-                  scale, dtype, 0.f, 0, 0, workspace, workspace_bytes, stream);
+                  0, scale, dtype, 0.f, 0, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_bwd_sink(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
+                void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int Hkv, int D, int causal,
+                int window_left, int window_right, int sinks, float scale, int dtype, void* workspace,
+                size_t workspace_bytes, cudaStream_t stream) {
+  return bwd_impl(-1, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right,
+                  sinks, scale, dtype, 0.f, 0, 0, workspace, workspace_bytes, stream);
 }
 
 int fa_bwd_dropout(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
@@ -504,7 +591,7 @@ int fa_bwd_dropout(const void* q, const void* k, const void* v, const void* out,
                    int window_left, int window_right, float scale, int dtype, float dropout_p, uint64_t seed,
                    uint32_t offset, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   return bwd_impl(-1, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, Hkv, D, causal, window_left, window_right,
-                  scale, dtype, dropout_p, seed, offset, workspace, workspace_bytes, stream);
+                  0, scale, dtype, dropout_p, seed, offset, workspace, workspace_bytes, stream);
 }
 
 int fa_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout, void* dq,

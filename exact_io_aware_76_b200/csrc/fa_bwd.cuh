@@ -48,6 +48,9 @@ struct BwdParams {
   int B, H, Sq, Sk, Sq_pad;  // H = query heads
   int Hkv, group;            // K/V heads and query heads per K/V head (H = Hkv * group)
   int win_left, win_right;   // window around the aligned key i + Sk - Sq; negative = unbounded side
+  int sinks;         // first keys that the window's left bound does not hide (kSink instances)
+  int sink_tiles, sink_pieces;  // key tiles that hold sinks; CTAs that share each one's queries
+  float* sink_part;  // sink_pieces > 1: fp32 partials [B*Hkv, sink_tiles, sink_pieces, dV / dK, 128, D]
   int n_kblk;        // ceil(Sk / 128)
   int units, n_grp;  // head dim 128: key tiles per CTA, CTAs per (batch, K/V head) = ceil(n_kblk / units)
   int head_major;    // CTA order: 1 = all key tiles of a head together (L2 reuse), 0 = heavy-first
@@ -161,6 +164,73 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const BwdParams p) {
   }
 }
 
+// ------------------------------------------------------------------------------------------ sinks
+// A key tile that holds sinks is seen by every later query, a window tile by about window / 128 query tiles only, so
+// for a long sequence one CTA per sink tile would run long after the others. The launch therefore deals a sink
+// tile's iterations (query tiles of every head of the group) to sink_pieces CTAs, which come first in the grid; with
+// more than one piece each leaves its fp32 dV and dK sums in the workspace, and fa_bwd_sink_sum adds them in piece
+// order (one order, so the results repeat bit for bit).
+// The work of CTA `block`: its (batch, K/V head), key tile and, for a sink tile, its piece; piece < 0 otherwise.
+struct SinkWork {
+  int bh, kblk, piece;
+};
+__device__ __forceinline__ SinkWork sink_work(const BwdParams& p, int block) {
+  const int n_bh = p.B * p.Hkv, per_bh = p.sink_tiles * p.sink_pieces;
+  SinkWork w;
+  if (block < n_bh * per_bh) {
+    w.bh = block / per_bh;
+    w.kblk = block % per_bh / p.sink_pieces;
+    w.piece = block % p.sink_pieces;
+  } else {
+    const int i = block - n_bh * per_bh, n = p.n_kblk - p.sink_tiles;
+    w.bh = p.head_major ? i / n : i % n_bh;
+    w.kblk = p.sink_tiles + (p.head_major ? i % n : i / n_bh);
+    w.piece = -1;
+  }
+  return w;
+}
+// Iterations [first, last) of piece `piece` out of n_it.
+__device__ __forceinline__ int sink_piece_begin(const BwdParams& p, int piece, int n_it) {
+  return static_cast<int>(static_cast<long long>(n_it) * piece / p.sink_pieces);
+}
+__device__ __forceinline__ float* sink_part_row(const BwdParams& p, const SinkWork& w, int which, int row, int D) {
+  const size_t tile = (static_cast<size_t>(w.bh) * p.sink_tiles + w.kblk) * p.sink_pieces + w.piece;
+  return p.sink_part + ((tile * 2 + which) * 128 + row) * D;
+}
+
+// dV and dK of the sink tiles from their pieces' partial sums; one thread per four values.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(256) fa_bwd_sink_sum_kernel(const BwdParams p) {
+  const long long n = static_cast<long long>(p.B) * p.Hkv * p.sink_tiles * 2 * 128 * (D / 4);
+  for (long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; t < n;
+       t += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int d = static_cast<int>(t % (D / 4)) * 4;
+    long long r = t / (D / 4);
+    const int row = static_cast<int>(r % 128);
+    r /= 128;
+    const int which = static_cast<int>(r % 2);
+    r /= 2;
+    SinkWork w;
+    w.kblk = static_cast<int>(r % p.sink_tiles);
+    w.bh = static_cast<int>(r / p.sink_tiles);
+    const int key = w.kblk * 128 + row;
+    if (key >= p.Sk) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (w.piece = 0; w.piece < p.sink_pieces; ++w.piece) {
+      const float4 x = *reinterpret_cast<const float4*>(sink_part_row(p, w, which, row, D) + d);
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    const float mul = which == 0 ? 1.f : p.scale;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(which == 0 ? p.dv : p.dk);
+    const int b = w.bh / p.Hkv, h_kv = w.bh % p.Hkv;
+    *reinterpret_cast<uint2*>(dst + ((static_cast<size_t>(b) * p.Sk + key) * p.Hkv + h_kv) * D + d) =
+        make_uint2(pack2<kBF16>(a.x * mul, a.y * mul), pack2<kBF16>(a.z * mul, a.w * mul));
+  }
+}
+
 // ------------------------------------------------------------------------------------------ main
 template <int D>
 struct BwdSmem {
@@ -203,7 +273,8 @@ __device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float 
 // dS^T staging buffer by it % NDS, stages of the Q/dO ring by it % NQS (four stages for D = 128: a Q/dO tile
 // takes longer to arrive than two tiles take to process); every barrier's phases are waited in order.
 // kDrop: attention dropout; a separate instance so the plain path keeps its registers.
-template <int D, bool kBF16, bool kCausal, bool kDrop = false>
+// kSink: a window bounded on the left whose first p.sinks keys stay visible (see SinkWork).
+template <int D, bool kBF16, bool kCausal, bool kDrop = false, bool kSink = false>
 __global__ void __launch_bounds__(384, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -231,8 +302,10 @@ __global__ void __launch_bounds__(384, 1)
   // A CTA owns one (batch, K/V head, key tile) and walks every query head of the K/V head's group, so the
   // group's dK/dV contributions accumulate in TMEM without any further reduction.
   const int n_bh = p.B * p.Hkv;
-  const int bh = p.head_major ? blockIdx.x / p.n_kblk : blockIdx.x % n_bh;  // (batch, K/V head)
-  const int kblk = p.head_major ? blockIdx.x % p.n_kblk : blockIdx.x / n_bh;
+  SinkWork sw;
+  if constexpr (kSink) sw = sink_work(p, blockIdx.x);
+  const int bh = kSink ? sw.bh : p.head_major ? blockIdx.x / p.n_kblk : blockIdx.x % n_bh;  // (batch, K/V head)
+  const int kblk = kSink ? sw.kblk : p.head_major ? blockIdx.x % p.n_kblk : blockIdx.x / n_bh;
   const int b = bh / p.Hkv, h_kv = bh % p.Hkv;
   const int off = p.Sk - p.Sq;
   const int key0 = kblk * 128;
@@ -243,10 +316,18 @@ __global__ void __launch_bounds__(384, 1)
   const int right = kCausal ? (p.win_right >= 0 ? min(p.win_right, 0) : 0) : p.win_right;
   const bool has_right = right >= 0;
   const int r_min = has_right ? max(0, key0 - off - right) : 0;
-  const int r_max = has_left ? min(p.Sq - 1, key1 - off + p.win_left) : p.Sq - 1;
+  const bool all_later = kSink && key0 < p.sinks;  // the tile holds sinks: every later query sees it
+  const int r_max = (has_left && !all_later) ? min(p.Sq - 1, key1 - off + p.win_left) : p.Sq - 1;
   const int i_begin = r_min / BQ;
   const int n_q = (r_max >= r_min) ? r_max / BQ - i_begin + 1 : 0;  // query tiles per head
-  const int n_it = n_q * p.group;                                     // iteration it: head it / n_q
+  int n_it = n_q * p.group;                                           // iteration it: head it / n_q
+  int it0 = 0;  // this CTA's first iteration (the pieces of a sink tile), counted from there below
+  if constexpr (kSink) {
+    if (sw.piece >= 0) {
+      it0 = sink_piece_begin(p, sw.piece, n_it);
+      n_it = sink_piece_begin(p, sw.piece + 1, n_it) - it0;
+    }
+  }
 
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
@@ -291,8 +372,8 @@ __global__ void __launch_bounds__(384, 1)
       int it = 0;
       for (; it < n_it; ++it) {
         const int s = it % NQS;
-        const int h = h_kv * p.group + it / n_q;
-        const int q0 = (i_begin + it % n_q) * BQ;
+        const int h = h_kv * p.group + (it0 + it) / n_q;
+        const int q0 = (i_begin + (it0 + it) % n_q) * BQ;
         const size_t row0 = (static_cast<size_t>(b) * p.H + h) * p.Sq_pad + q0;
         if (it >= NQS && !mbar_wait(&q_empty[s], ((it / NQS) - 1) & 1, abort_flag)) break;
         mbar_arrive_expect_tx(&q_full[s], 2 * L::kQBytes + 2 * BQ * 4);
@@ -404,7 +485,7 @@ __global__ void __launch_bounds__(384, 1)
     // are masked outside [lo_c, hi_c].
     for (int it = 0; it < n_it; ++it) {
       const int x = it % NB, s = it % NQS;
-      const int q0 = (i_begin + it % n_q) * BQ;
+      const int q0 = (i_begin + (it0 + it) % n_q) * BQ;
       if (!mbar_wait(&sdp_full[x], (it / NB) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after_sync();
       const float* lse2 = reinterpret_cast<const float*>(smem + L::kLOff + s * BQ * 4);
@@ -414,9 +495,10 @@ __global__ void __launch_bounds__(384, 1)
       uint8_t* ds_row_base = smem + L::kDSOff + (it % L::kNDS) * L::kDSBytes + j * 128;
       const uint32_t s_col = L::kColS + x * BQ, dp_col = L::kColDP + x * BQ;
       const int lo_c = has_right ? key - off - right - q0 : -1;
-      const int hi_c = has_left ? key - off + p.win_left - q0 : BQ;
+      const int hi_c = (has_left && !(kSink && key < p.sinks)) ? key - off + p.win_left - q0 : BQ;
       // Whole tile visible to every key of this CTA: no element mask.
-      const bool need_mask = (has_right && key0 + 127 - off - right > q0) || (has_left && key0 - off + p.win_left < q0 + BQ - 1);
+      const bool need_mask = (has_right && key0 + 127 - off - right > q0) ||
+                             (has_left && !(kSink && key0 + 127 < p.sinks) && key0 - off + p.win_left < q0 + BQ - 1);
       if constexpr (kDrop) {
         // One 64-query chunk; with dropout (kDrop) the mask's bytes for the chunk come first: per 16 queries the
         // four lanes of this key's 4-key block each generate one 4x4 block, transpose its bytes (word = key) and
@@ -552,6 +634,14 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = 0.f;
           }
+          if constexpr (kSink) {
+            if (sw.piece >= 0 && p.sink_pieces > 1) {
+              float4* part = reinterpret_cast<float4*>(sink_part_row(p, sw, which, j, D) + c0);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) part[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              continue;
+            }
+          }
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) w[c / 2] = pack2<kBF16>(v[c] * mul, v[c + 1] * mul);
@@ -574,8 +664,8 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_base = tmem + ((quarter * 32) << 16);
     for (int it = 0; it < n_it; ++it) {
       const int x = it % NB;
-      const int h = h_kv * p.group + it / n_q;
-      const int q0 = (i_begin + it % n_q) * BQ;
+      const int h = h_kv * p.group + (it0 + it) / n_q;
+      const int q0 = (i_begin + (it0 + it) % n_q) * BQ;
       const size_t row0 = (static_cast<size_t>(b) * p.H + h) * p.Sq_pad + q0;
       if (!mbar_wait(&dq_full[x], (it / NB) & 1, abort_flag)) break;
       tc_fence_after_sync();

@@ -60,7 +60,7 @@ struct Bwd128Smem {
 // the per-instruction descriptors from them where they are used instead of keeping all of them live.
 __device__ __forceinline__ void opaque(uint64_t& a, uint64_t& b) { asm volatile("" : "+l"(a), "+l"(b)); }
 
-template <bool kBF16, bool kCausal, bool kDrop = false>
+template <bool kBF16, bool kCausal, bool kDrop = false, bool kSink = false>
 __global__ void __launch_bounds__(512, 1)
     fa_bwd_main128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -100,33 +100,44 @@ __global__ void __launch_bounds__(512, 1)
   // alternately from both ends (0, n-1, 1, n-2, ...), so every CTA gets about the same number of query tiles.
   // CTA order: head-major for large problems (the units of one (batch, K/V head) together), so that its Q, dO
   // and dQ accumulator stay in L2; otherwise across heads. With one unit per CTA the key tiles run heavy-first.
+  // With sinks (see SinkWork) a CTA takes one key tile, or a piece of one that holds sinks.
   const int n_bh = p.B * p.Hkv;
-  const int bh = p.head_major ? blockIdx.x / p.n_grp : blockIdx.x % n_bh;
-  const int grp = p.head_major ? blockIdx.x % p.n_grp : blockIdx.x / n_bh;
+  SinkWork sw;
+  if constexpr (kSink) sw = sink_work(p, blockIdx.x);
+  const int bh = kSink ? sw.bh : p.head_major ? blockIdx.x / p.n_grp : blockIdx.x % n_bh;
+  const int grp = kSink ? sw.kblk : p.head_major ? blockIdx.x % p.n_grp : blockIdx.x / n_bh;
   const int b = bh / p.Hkv, h_kv = bh % p.Hkv;
   const int off = p.Sk - p.Sq;
-  const int n_units = max(0, min(p.units, p.n_kblk - grp * p.units));
+  const int n_units = kSink ? 1 : max(0, min(p.units, p.n_kblk - grp * p.units));
   // Query r sees key j iff r + off - left <= j <= r + off + right (causal caps right at 0; negative bounds are
   // unbounded), i.e. j - off - right <= r <= j - off + left.
   const bool has_left = p.win_left >= 0;
   const int right = kCausal ? (p.win_right >= 0 ? min(p.win_right, 0) : 0) : p.win_right;
   const bool has_right = right >= 0;
   // Unit u: key tile, its query tiles [i_begin, i_begin + n_q) per head, n_it = n_q * group iterations
-  // (iteration it: head it / n_q).
+  // (iteration it: head (it0 + it) / n_q; it0 > 0 in the later pieces of a sink tile only).
   struct Unit {
-    int key0, i_begin, n_q, n_it;
+    int key0, i_begin, n_q, n_it, it0;
   };
   auto unit_at = [&](int u) {
-    const int i = grp * p.units + u;
-    const int kblk = p.units == 1 ? i : ((i & 1) ? p.n_kblk - 1 - i / 2 : i / 2);
+    const int i = kSink ? grp : grp * p.units + u;
+    const int kblk = (kSink || p.units == 1) ? i : ((i & 1) ? p.n_kblk - 1 - i / 2 : i / 2);
     Unit U;
     U.key0 = kblk * 128;
     const int key1 = min(p.Sk - 1, U.key0 + 127);
     const int r_min = has_right ? max(0, U.key0 - off - right) : 0;
-    const int r_max = has_left ? min(p.Sq - 1, key1 - off + p.win_left) : p.Sq - 1;
+    const bool all_later = kSink && U.key0 < p.sinks;  // the tile holds sinks: every later query sees it
+    const int r_max = (has_left && !all_later) ? min(p.Sq - 1, key1 - off + p.win_left) : p.Sq - 1;
     U.i_begin = r_min / BQ;
     U.n_q = (r_max >= r_min) ? r_max / BQ - U.i_begin + 1 : 0;
     U.n_it = U.n_q * p.group;
+    U.it0 = 0;
+    if constexpr (kSink) {
+      if (sw.piece >= 0) {
+        U.it0 = sink_piece_begin(p, sw.piece, U.n_it);
+        U.n_it = sink_piece_begin(p, sw.piece + 1, U.n_it) - U.it0;
+      }
+    }
     return U;
   };
 
@@ -170,8 +181,8 @@ __global__ void __launch_bounds__(512, 1)
       // Q, dO, LSE2 and D of global iteration gi (counted over this CTA's units) into stage gi % NQS.
       auto load_q = [&](int gi, const Unit& U, int it) -> bool {
         const int s = gi % NQS;
-        const int h = h_kv * p.group + it / U.n_q;
-        const int q0 = (U.i_begin + it % U.n_q) * BQ;
+        const int h = h_kv * p.group + (U.it0 + it) / U.n_q;
+        const int q0 = (U.i_begin + (U.it0 + it) % U.n_q) * BQ;
         const size_t row0 = (static_cast<size_t>(b) * p.H + h) * p.Sq_pad + q0;
         if (gi >= NQS && !mbar_wait(&q_empty[s], ((gi / NQS) - 1) & 1, abort_flag)) return false;
         mbar_arrive_expect_tx(&q_full[s], 2 * L::kTile + 2 * BQ * 4);
@@ -356,15 +367,16 @@ __global__ void __launch_bounds__(512, 1)
       for (int it = 0; it < n_it; ++it) {
         const int gi = g + it;
         const int s = gi % NQS;
-        const int q0 = (i_begin + it % n_q) * BQ;
+        const int q0 = (i_begin + (U.it0 + it) % n_q) * BQ;
         const float* lse2 = reinterpret_cast<const float*>(smem_raw + L::kLOff + s * BQ * 4) + cb;
         const float* dvec = reinterpret_cast<const float*>(smem_raw + L::kDVecOff + s * BQ * 4) + cb;
         // This key's visible queries are [key - off - right, key - off + left]: columns (tile-relative) outside
         // [lo_c, hi_c] are masked; a tile every key of this CTA sees whole needs no element mask.
         const int lo_c = has_right ? key - off - right - q0 : -1;
-        const int hi_c = has_left ? key - off + p.win_left - q0 : BQ;
+        const int hi_c = (has_left && !(kSink && key < p.sinks)) ? key - off + p.win_left - q0 : BQ;
         const bool need_mask =
-            (has_right && key0 + 127 - off - right > q0) || (has_left && key0 - off + p.win_left < q0 + BQ - 1);
+            (has_right && key0 + 127 - off - right > q0) ||
+            (has_left && !(kSink && key0 + 127 < p.sinks) && key0 - off + p.win_left < q0 + BQ - 1);
         // ---- P^T from S^T (64 columns of this warpgroup), kept in fp32 for dS^T; 16-bit P^T (times the keep
         // mask with dropout) back into TMEM over the first 32 of these columns. The dropout mask is generated
         // first, while S^T may still be in flight.
@@ -490,6 +502,15 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[c] = 0.f;
             }
+            if constexpr (kSink) {
+              if (sw.piece >= 0 && p.sink_pieces > 1) {
+                float4* part = reinterpret_cast<float4*>(sink_part_row(p, sw, which, j, 128) + cb + c0);
+#pragma unroll
+                for (int q4 = 0; q4 < 8; ++q4)
+                  part[q4] = make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+                continue;
+              }
+            }
             uint32_t wd[16];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) wd[c / 2] = pack2<kBF16>(v[c] * mul, v[c + 1] * mul);
@@ -501,6 +522,7 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
           __syncwarp();
+          if (kSink && sw.piece >= 0 && p.sink_pieces > 1) continue;  // the pieces' sums are joined afterwards
           uint16_t* dst = reinterpret_cast<uint16_t*>(which == 0 ? p.dv : p.dk);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -529,8 +551,8 @@ __global__ void __launch_bounds__(512, 1)
       const Unit U = unit_at(u);
       for (int it = 0; it < U.n_it; ++it) {
         const int gi = g + it;
-        const int h = h_kv * p.group + it / U.n_q;
-        const int q0 = (U.i_begin + it % U.n_q) * BQ;
+        const int h = h_kv * p.group + (U.it0 + it) / U.n_q;
+        const int q0 = (U.i_begin + (U.it0 + it) % U.n_q) * BQ;
         if (!mbar_wait(dq_full, gi & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
         float v[128];

@@ -43,6 +43,7 @@ struct FwdParams {
   int B, H, Sq, Sk;    // H = query heads
   int Hkv, group;      // K/V heads and query heads per K/V head (H = Hkv * group)
   int win_left, win_right;  // window around the aligned key i + Sk - Sq; negative = unbounded side
+  int sinks;       // first keys that the window's left bound does not hide (kSink instances; 0 < sinks < Sk)
   int n_qblk;      // ceil(Sq / 256)
   int n_kv_total;  // ceil(Sk / 128)
   int head_major;  // CTA order: 1 = all query blocks of a head together (K/V reuse in L2), 0 = heavy-first
@@ -92,7 +93,10 @@ struct FwdSmem {
 
 // kBF16: the 16-bit input type (and output type); with kFP8 the inputs are e4m3 and the output is bf16.
 // kDrop: attention dropout (16-bit inputs only); a separate instance so the plain path keeps its registers.
-template <int D, bool kBF16, bool kCausal, bool kFP8 = false, bool kDrop = false>
+// kSink: a window bounded on the left whose first p.sinks keys stay visible. The CTA then walks the window's key
+// tiles and the few tiles before them that hold sinks, and skips everything between: the work per query is that of
+// left + sinks keys whatever the length.
+template <int D, bool kBF16, bool kCausal, bool kFP8 = false, bool kDrop = false, bool kSink = false>
 __global__ void __launch_bounds__(384, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -156,7 +160,31 @@ __global__ void __launch_bounds__(384, 1)
     j_begin = min(j_lo[0], j_lo[1]);
     j_end = max(j_lo[0] + n_kv[0], j_lo[1] + n_kv[1]);
   }
-  const int n_iter = j_end - j_begin;
+  // The walk: steps 0 .. n_iter-1, each one key tile; Q tile t takes part in the n_kv[t] steps from w_lo[t] on.
+  // Sink tiles [0, n_sink) before the window are inserted at step w_sink, where tile 1's window begins: tile 0
+  // still has its last window tiles to come there, so both Q tiles keep one unbroken run of steps.
+  int n_iter = j_end - j_begin, n_sink = 0, w_sink = 0;
+  if constexpr (kSink) {
+    if (n_iter > 0) {
+      const int n_tiles = (p.sinks + 127) / 128;
+      n_sink = min(n_tiles, j_begin);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (n_kv[t] > 0 && n_tiles > j_begin) {  // the sinks reach into the walked tiles: tile 1 starts there too
+          n_kv[t] += j_lo[t] - j_begin;
+          j_lo[t] = j_begin;
+        }
+      w_sink = (n_kv[0] > 0 && n_kv[1] > 0) ? j_lo[1] - j_begin : 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) n_kv[t] += n_kv[t] > 0 ? n_sink : 0;
+      n_iter += n_sink;
+    }
+  }
+  const int w_lo[2] = {j_lo[0] - j_begin, j_lo[1] - j_begin};
+  auto key_tile = [&](int w) {
+    if (!kSink || w < w_sink) return j_begin + w;
+    return w < w_sink + n_sink ? w - w_sink : j_begin + w - n_sink;
+  };
 
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
@@ -203,10 +231,10 @@ __global__ void __launch_bounds__(384, 1)
           tma_load_4d(smem + L::kQOff + t * L::kTileBytes + c * 16384, &tm_q, q_full, L::kChunkElems * c, h,
                       qblk * 256 + t * 128, b);
       }
-      int j = 0;  // index into the CTA's key tiles; the key tile is j_begin + j
+      int j = 0;  // step of the CTA's walk over key tiles
       for (; j < n_iter; ++j) {
         const int s = j % L::kStages;
-        const int key0 = (j_begin + j) * 128;
+        const int key0 = key_tile(j) * 128;
         if (j >= L::kStages && !mbar_wait(&kv_empty[s], ((j / L::kStages) - 1) & 1, abort_flag)) break;
         mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
         for (int c = 0; c < L::kChunks; ++c)
@@ -272,16 +300,15 @@ __global__ void __launch_bounds__(384, 1)
             umma_ts(o_tmem, p_tmem + kk * 8, sdesc_add(b0, kk * kKeys * 128), idesc_pv, (acc || kk > 0) ? 1u : 0u);
         }
       };
-      // Key tile jj (local index j = jj - j_begin) serves Q tile t when j_lo[t] <= jj < j_lo[t] + n_kv[t]; a
-      // tile's first S is issued when the walk reaches its interval, every later one right after its PV.
+      // Step j serves Q tile t when w_lo[t] <= j < w_lo[t] + n_kv[t]; a tile's first S is issued when the walk
+      // reaches its run of steps, every later one right after its PV.
       for (int j = 0; ok && j < n_iter; ++j) {
-        const int jj = j_begin + j;
         const int s = j % L::kStages;
         const uint32_t ph = (j / L::kStages) & 1;
         if (!mbar_wait(&k_full[s], ph, abort_flag)) break;
         tc_fence_after_sync();
         for (int t = 0; t < 2; ++t)
-          if (n_kv[t] > 0 && jj == j_lo[t]) {
+          if (n_kv[t] > 0 && j == w_lo[t]) {
             issue_qk(t, s);
             umma_commit(&s_full[t]);
           }
@@ -289,8 +316,8 @@ __global__ void __launch_bounds__(384, 1)
         const int jn = j + 1;
         bool next_k_ready = false;
         for (int t = 0; t < 2 && ok; ++t) {
-          if (n_kv[t] == 0 || jj < j_lo[t] || jj >= j_lo[t] + n_kv[t]) continue;
-          const int u = jj - j_lo[t];  // this tile's local step
+          if (n_kv[t] == 0 || j < w_lo[t] || j >= w_lo[t] + n_kv[t]) continue;
+          const int u = j - w_lo[t];  // this tile's local step
           if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
           issue_pv(t, s, u > 0, 0);
@@ -348,12 +375,13 @@ __global__ void __launch_bounds__(384, 1)
       tc_fence_after_sync();
       float s[128];
       tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(s));
-      const int key0 = (j_lo[t] + j) * 128;
-      const bool need_mask = key0 < all_lo || key0 + 127 > all_hi;
+      const int key0 = key_tile(w_lo[t] + j) * 128;
+      const bool need_mask =
+          (key0 < all_lo && (!kSink || key0 + 127 >= p.sinks)) || key0 + 127 > all_hi;
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
-          if (key0 + c < row_lo || key0 + c > row_hi) s[c] = masked;
+          if ((key0 + c < row_lo && (!kSink || key0 + c >= p.sinks)) || key0 + c > row_hi) s[c] = masked;
       }
       // The row's largest s*c: c times the largest score for c > 0, times the smallest for c < 0. Four
       // independent chains of three-input maxima (minima), then combined.

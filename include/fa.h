@@ -88,6 +88,19 @@ FA_API int fa_fwd_ex(const void* q, const void* k, const void* v, void* out, flo
                      cudaStream_t stream);
 
 /*
+ * Forward with a sliding window and sinks: the first `sinks` keys stay visible to every query although the window's
+ * left bound hides them (a decoder with a bounded window keeps its first tokens in sight; beyond the pages).
+ *   sinks >= 0 (FA_ERR_INVALID if negative): with c = i + Sk - Sq, key j is visible iff
+ *   (window_left < 0 or j >= c - window_left or j < sinks) and (window_right < 0 or j <= c + window_right), on top of
+ *   the causal rule. The right bound and the causal rule hold for sinks too.
+ * sinks = 0 or window_left < 0 is exactly fa_fwd_ex. K and V must be finite: a non-finite value of a masked key may
+ * reach the rows that share its 128-key tile. Other arguments, conventions and errors as fa_fwd_ex.
+ */
+FA_API int fa_fwd_sink(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Sq, int Sk,
+                       int H, int Hkv, int D, int causal, int window_left, int window_right, int sinks, float scale,
+                       int dtype, cudaStream_t stream);
+
+/*
  * Forward with attention dropout (the `dropout_p` argument of the skill page's flash_attn_func call, Workflow 2
  * Step 2; the pages name it only). Arguments as fa_fwd_ex, plus:
  *   dropout_p  drop probability, 0 <= dropout_p < 1; it is rounded to t / 256 with t = floor(256 p + 1/2), and
@@ -152,6 +165,23 @@ FA_API int fa_bwd_ex(const void* q, const void* k, const void* v, const void* ou
                      const void* dout, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int Hkv, int D,
                      int causal, int window_left, int window_right, float scale, int dtype, void* workspace,
                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace fa_bwd_sink needs (0 on invalid sizes): fa_bwd's, plus fp32 partial sums of the sinks' dK
+ * and dV where the queries that see them are split over several CTAs.
+ */
+FA_API size_t fa_bwd_sink_workspace_size(int B, int Sq, int Sk, int H, int Hkv, int D, int causal, int window_left,
+                                         int window_right, int sinks);
+
+/*
+ * Backward of fa_fwd_sink: arguments as fa_bwd_ex plus the forward's sinks; the workspace holds
+ * fa_bwd_sink_workspace_size(...) bytes of the same arguments. dK and dV repeat bit for bit; dQ's fp32 reductions may
+ * land in another order, as in fa_bwd.
+ */
+FA_API int fa_bwd_sink(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                       const void* dout, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int Hkv, int D,
+                       int causal, int window_left, int window_right, int sinks, float scale, int dtype,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * The three launches of fa_bwd one at a time, for callers that time or schedule them separately:
