@@ -7,6 +7,9 @@ no fallback: if the library is missing or fails to load, every call raises.
     fwd(q, k, v, causal=False, scale=None, window=(-1, -1), sinks=0) -> (out, lse)
     bwd(q, k, v, out, lse, dout, causal=False, scale=None, window=(-1, -1), sinks=0) -> (dq, dk, dv)
 
+    cache_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, counts=None)
+    fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, window_left=-1, sinks=0) -> (out, lse)
+
 Layouts follow the C header (include/fa.h): q/out/dout [B, Sq, H, D], k/v [B, Sk, Hkv, D] (Hkv divides H:
 grouped or multi-query K/V heads), fp16 or bf16, contiguous, on one CUDA device; lse is fp32 [B, H, Sq].
 ``scale=None`` means 1/sqrt(D); ``window=(left, right)`` limits each query to keys within left before and
@@ -28,7 +31,7 @@ STATUS_NAMES = {0: "FA_OK", -1: "FA_ERR_INVALID", -2: "FA_ERR_UNSUPPORTED", -3: 
                 -4: "FA_ERR_TIMEOUT", -5: "FA_ERR_WORKSPACE"}
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_dropout", "fa_fwd_sink", "fa_bwd_dropout", "fa_bwd",
            "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace_size", "fa_bwd_stage", "fa_bwd_noalloc",
-           "fa_bwd_workspace_size", "fa_status_string", "fa_device_status")
+           "fa_bwd_workspace_size", "fa_cache_append", "fa_cache_fwd", "fa_cache_workspace_size", "fa_status_string", "fa_device_status")
 
 _lib = None
 
@@ -75,6 +78,12 @@ def lib():
     L.fa_bwd_sink.argtypes = [vp] * 9 + [i] * 10 + [f, i, vp, sz, vp]
     L.fa_bwd_sink_workspace_size.restype = sz
     L.fa_bwd_sink_workspace_size.argtypes = [i] * 10
+    L.fa_cache_append.restype = i
+    L.fa_cache_append.argtypes = [vp] * 9 + [i] * 8 + [vp]
+    L.fa_cache_workspace_size.restype = sz
+    L.fa_cache_workspace_size.argtypes = [i] * 5
+    L.fa_cache_fwd.restype = i
+    L.fa_cache_fwd.argtypes = [vp] * 9 + [i] * 10 + [f, i, vp, sz, vp]
     L.fa_bwd_workspace_size.restype = sz
     L.fa_bwd_workspace_size.argtypes = [i, i, i, i]
     L.fa_status_string.restype = ctypes.c_char_p
@@ -159,6 +168,33 @@ def check_sinks(sinks, dropout_p):
         raise ValueError("sinks must be a number of keys (a 32-bit integer >= 0), got %r" % (sinks,))
     if sinks and dropout_p:
         raise ValueError("sinks and dropout do not go together")
+
+
+def check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev):
+    """The cache's operands against B sequences, Hkv heads of D. Returns (num_pages, page, max_pages)."""
+    import torch
+
+    if len(k_pages.shape) != 4 or k_pages.shape[1] != Hkv or k_pages.shape[3] != D:
+        raise ValueError("k_pages must be [num_pages, Hkv=%s, page, D=%d], got %s" % (Hkv, D, tuple(k_pages.shape)))
+    num_pages, page = k_pages.shape[0], k_pages.shape[2]
+    if page not in (16, 32, 64, 128):
+        raise ValueError("a page must hold 16, 32, 64 or 128 tokens, got %d" % page)
+    _check("k_pages", k_pages, dev, dtype=torch.float8_e4m3fn)
+    _check("v_pages", v_pages, dev, shape=k_pages.shape, dtype=torch.float8_e4m3fn)
+    _check("k_scale", k_scale, dev, shape=(num_pages, Hkv), dtype=torch.float32)
+    _check("v_scale", v_scale, dev, shape=(num_pages, Hkv), dtype=torch.float32)
+    if len(table.shape) != 2 or table.shape[0] != B:
+        raise ValueError("table must be [B=%d, max_pages], got %s" % (B, tuple(table.shape)))
+    _check("table", table, dev, dtype=torch.int32)
+    _check("lens", lens, dev, shape=(B,), dtype=torch.int32)
+    return num_pages, page, table.shape[1]
+
+
+def _used_on(stream, *tensors):
+    """Tensors made here (on the current stream) whose memory a call on another stream still uses after it returns."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
 
 
 def _stream(stream, dev):
@@ -304,6 +340,85 @@ def bwd_noalloc(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=N
     if rc != FA_OK:
         raise FAError(rc, "fa_bwd_noalloc")
     return dq, dk, dv
+
+
+def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, counts=None, stream=None):
+    """Rounds new tokens to e4m3 and writes them into a paged cache (``fa_cache_append`` in include/fa.h).
+
+    k, v [B, T, Hkv, D] fp16 or bf16; k_pages, v_pages [num_pages, Hkv, page, D] float8_e4m3fn; k_scale, v_scale
+    [num_pages, Hkv] fp32; table [B, max_pages] and lens [B] int32: page numbers, and lengths with the new tokens.
+    The last ``counts[b]`` (int32 [B]; default T) of sequence b's rows are its new tokens. The cache is changed in place."""
+    import torch
+
+    dev = getattr(k, "device", None)
+    if dev is None or dev.type != "cuda" or len(k.shape) != 4:
+        raise ValueError("k must be a [B, T, Hkv, D] CUDA tensor")
+    if k.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("k must be float16 or bfloat16, got %s" % k.dtype)
+    B, T, Hkv, D = k.shape
+    _check("k", k, dev)
+    _check("v", v, dev, shape=k.shape, dtype=k.dtype)
+    num_pages, page, max_pages = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
+    if counts is not None:
+        _check("counts", counts, dev, shape=(B,), dtype=torch.int32)
+    with _device(dev):
+        rc = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                   k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                   None if counts is None else counts.data_ptr(), B, T, Hkv, D, num_pages, page,
+                                   max_pages, _dtype_code(k), _stream(stream, dev))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_cache_append")
+
+
+def cache_workspace_size(B, Sq, H, Hkv, D):
+    return int(lib().fa_cache_workspace_size(B, Sq, H, Hkv, D))
+
+
+def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, window_left=-1, sinks=0, out=None,
+              lse=None, workspace=None, stream=None):
+    """Attention of each sequence's last Sq tokens over a paged e4m3 cache (``fa_cache_fwd`` in include/fa.h).
+
+    q [B, Sq, H, D] fp16 or bf16; the cache as in ``cache_append``. Causal; ``window_left`` >= 0 hides keys more than
+    that far before a query's own, except the first ``sinks``. Returns (out [B,Sq,H,D], lse fp32 [B,H,Sq])."""
+    import torch
+
+    dev = getattr(q, "device", None)
+    if dev is None or dev.type != "cuda" or len(q.shape) != 4:
+        raise ValueError("q must be a [B, Sq, H, D] CUDA tensor")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("q must be float16 or bfloat16, got %s" % q.dtype)
+    _check("q", q, dev)
+    B, Sq, H, D = q.shape
+    Hkv = k_pages.shape[1] if len(k_pages.shape) == 4 else 0
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError("the K/V head count %d must divide the query head count %d" % (Hkv, H))
+    num_pages, page, max_pages = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
+    check_sinks(sinks, 0.0)
+    with _device(dev):
+        made = []
+        if out is None:
+            out = torch.empty_like(q)
+            made.append(out)
+        if lse is None:
+            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+            made.append(lse)
+        check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
+        ws_bytes = cache_workspace_size(B, Sq, H, Hkv, D)
+        if workspace is None:
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+            made.append(workspace)
+        _check("workspace", workspace, dev)
+        if workspace.numel() * workspace.element_size() < ws_bytes:
+            raise ValueError("workspace must hold at least %d bytes" % ws_bytes)
+        rc = lib().fa_cache_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                B, Sq, H, Hkv, D, num_pages, page, max_pages, int(window_left), int(sinks),
+                                float(0.0 if scale is None else scale), _dtype_code(q), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream, dev))
+        _used_on(stream, *made)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_cache_fwd")
+    return out, lse
 
 
 def device_status(reset=False, device=None):

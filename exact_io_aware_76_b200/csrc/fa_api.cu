@@ -8,6 +8,7 @@
 #include "fa.h"
 #include "fa_bwd.cuh"
 #include "fa_bwd128.cuh"
+#include "fa_cache.cuh"
 #include "fa_fwd.cuh"
 
 namespace {
@@ -599,6 +600,201 @@ int fa_bwd(const void* q, const void* k, const void* v, const void* out, const f
            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   return fa_bwd_stage(-1, q, k, v, out, lse, dout, dq, dk, dv, B, Sq, Sk, H, D, causal, scale, dtype, workspace,
                       workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------------ paged cache
+namespace {
+using fa::AppendParams;
+using fa::CacheParams;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The cache's own sizes and pointers. Rows of the [num_pages * Hkv * page, D] view are 32-bit TMA coordinates.
+int check_cache(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale, const int* table,
+                const int* lens, int B, int Hkv, int D, int num_pages, int page, int max_pages) {
+  if (B < 1 || Hkv < 1 || D < 1 || num_pages < 1 || max_pages < 1) return FA_ERR_INVALID;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_INVALID;
+  if ((double)num_pages * Hkv * page > 2147483392.0 || (double)max_pages * page > 1073741824.0) return FA_ERR_INVALID;
+  if (!k_pages || !v_pages || !k_scale || !v_scale || !table || !lens) return FA_ERR_INVALID;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(table) ||
+      !aligned4(lens))
+    return FA_ERR_INVALID;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int encode_pages_map(CUtensorMap* m, const void* base, int num_pages, int Hkv, int page, int D) {
+  auto enc = encode_fn();
+  if (!enc) return FA_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)num_pages * Hkv * page};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {128, (cuuint32_t)page};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+constexpr int kFewRows = 32, kManyRows = 256;
+struct CacheLayout {
+  size_t ml, cuts, total;
+};
+CacheLayout cache_layout(int rows, int D) {
+  CacheLayout l;
+  const size_t slots = (size_t)fa::kCacheCtas * 2 * rows;
+  l.ml = align256(slots * D * sizeof(float));
+  l.cuts = l.ml + align256(slots * 2 * sizeof(float));
+  l.total = l.cuts + align256(fa::kCacheCtas * sizeof(int4));
+  return l;
+}
+int check_cache_queries(int B, int Sq, int H, int Hkv, int D) {
+  if (B < 1 || Sq < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || D < 1) return FA_ERR_INVALID;
+  if ((double)B * Sq * H * D > 4.0e12 || (double)Sq * (H / Hkv) > 1073741824.0 ||
+      (double)B * (((double)Sq * (H / Hkv) + 255) / 256) > 1073741824.0)
+    return FA_ERR_INVALID;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+template <int D, bool BF16, bool FEW>
+int launch_cache(const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams& p, bool join, int dev,
+                 cudaStream_t stream) {
+  using L = fa::CacheSmem<D, BF16, FEW>;
+  static bool attr_done[kMaxDevices] = {};
+  if constexpr (FEW) {
+    auto kern = fa::fa_cache_few_kernel<D, BF16>;
+    int rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done);
+    if (rc) return rc;
+    kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
+  } else {
+    auto kern = fa::fa_cache_many_kernel<D, BF16>;
+    int rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done);
+    if (rc) return rc;
+    kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
+  }
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (join) {
+    fa::fa_cache_join_kernel<D, BF16, L::kRows><<<fa::kCacheCtas, 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+template <int D, bool BF16>
+int dispatch_cache(bool few, const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams& p, bool join, int dev,
+                   cudaStream_t s) {
+  return few ? launch_cache<D, BF16, true>(tk, tv, p, join, dev, s)
+             : launch_cache<D, BF16, false>(tk, tv, p, join, dev, s);
+}
+
+template <int D, bool BF16>
+int launch_append(const AppendParams& p, long long ctas, cudaStream_t stream) {
+  fa::fa_cache_append_kernel<D, BF16><<<(unsigned)ctas, 128, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                    const int* table, const int* lens, const int* counts, int B, int T, int Hkv, int D, int num_pages,
+                    int page, int max_pages, int dtype, cudaStream_t stream) {
+  if (T < 1 || !k || !v || !aligned16(k) || !aligned16(v) || !aligned4(counts)) return FA_ERR_INVALID;
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_INVALID;
+  int rc = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, num_pages, page, max_pages);
+  if (rc) return rc;
+  if ((double)B * T * Hkv * D > 4.0e12) return FA_ERR_INVALID;
+  AppendParams p;
+  p.n_touch = (T - 1 + page - 1) / page + 1;
+  if (p.n_touch > max_pages) p.n_touch = max_pages;
+  const double ctas = 2.0 * B * Hkv * p.n_touch;
+  if (ctas > 2147483647.0) return FA_ERR_INVALID;
+  int dev = 0;
+  if ((rc = current_device(&dev))) return rc;
+  p.k = k;
+  p.v = v;
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = table;
+  p.lens = lens;
+  p.counts = counts;
+  p.B = B;
+  p.T = T;
+  p.Hkv = Hkv;
+  p.page = page;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  const long long n = (long long)ctas;
+  if (D == 64)
+    return dtype == FA_BF16 ? launch_append<64, true>(p, n, stream) : launch_append<64, false>(p, n, stream);
+  return dtype == FA_BF16 ? launch_append<128, true>(p, n, stream) : launch_append<128, false>(p, n, stream);
+}
+
+size_t fa_cache_workspace_size(int B, int Sq, int H, int Hkv, int D) {
+  if (check_cache_queries(B, Sq, H, Hkv, D) != FA_OK) return 0;
+  return cache_layout(Sq * (H / Hkv) <= kFewRows ? kFewRows : kManyRows, D).total;
+}
+
+int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                 const int* table, const int* lens, void* out, float* lse, int B, int Sq, int H, int Hkv, int D,
+                 int num_pages, int page, int max_pages, int window_left, int sinks, float scale, int dtype,
+                 void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned4(lse)) return FA_ERR_INVALID;
+  if (!isfinite(scale) || sinks < 0 || (dtype != FA_F16 && dtype != FA_BF16)) return FA_ERR_INVALID;
+  int rc = check_cache_queries(B, Sq, H, Hkv, D);
+  if (rc == FA_OK)
+    rc = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, num_pages, page, max_pages);
+  if (rc) return rc;
+  const int capacity = max_pages * page, n_rows = Sq * (H / Hkv);
+  const bool few = n_rows <= kFewRows;
+  const int rows = few ? kFewRows : kManyRows;
+  const int n_mt = (n_rows + rows - 1) / rows;
+  if ((double)B * n_mt * Hkv * (capacity / 128 + 2) > 2147483647.0 * fa::kCacheCtas) return FA_ERR_INVALID;
+  const CacheLayout lay = cache_layout(rows, D);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < lay.total)
+    return FA_ERR_WORKSPACE;
+  int dev = 0;
+  if ((rc = current_device(&dev))) return rc;
+  if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  CUtensorMap tk, tv;
+  if ((rc = encode_pages_map(&tk, k_pages, num_pages, Hkv, page, D))) return rc;
+  if ((rc = encode_pages_map(&tv, v_pages, num_pages, Hkv, page, D))) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  CacheParams p;
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = table;
+  p.lens = lens;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
+  p.cuts = reinterpret_cast<int4*>(ws + lay.cuts);
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.group = H / Hkv;
+  p.Sq = Sq;
+  p.n_rows = n_rows;
+  p.n_mt = n_mt;
+  p.page = page;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  // A window as long as the cache hides nothing; without a window every key is visible and sinks change nothing.
+  p.win_left = (window_left < 0 || window_left >= capacity) ? -1 : window_left;
+  p.sinks = p.win_left < 0 ? 0 : sinks < capacity ? sinks : capacity;
+  p.scale_log2 = scale * fa::kLog2e;
+  const bool join = capacity > 128;  // units of one tile are never cut
+  if (D == 64)
+    return dtype == FA_BF16 ? dispatch_cache<64, true>(few, tk, tv, p, join, dev, stream)
+                            : dispatch_cache<64, false>(few, tk, tv, p, join, dev, stream);
+  return dtype == FA_BF16 ? dispatch_cache<128, true>(few, tk, tv, p, join, dev, stream)
+                          : dispatch_cache<128, false>(few, tk, tv, p, join, dev, stream);
 }
 
 }  // extern "C"

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(384, 1)
   // A CTA owns one (batch, K/V head, key tile) and walks every query head of the K/V head's group, so the
   // group's dK/dV contributions accumulate in TMEM without any further reduction.
   const int n_bh = p.B * p.Hkv;
-  SinkWork sw;
+  SinkWork sw{};
   if constexpr (kSink) sw = sink_work(p, blockIdx.x);
   const int bh = kSink ? sw.bh : p.head_major ? blockIdx.x / p.n_kblk : blockIdx.x % n_bh;  // (batch, K/V head)
   const int kblk = kSink ? sw.kblk : p.head_major ? blockIdx.x % p.n_kblk : blockIdx.x / n_bh;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(512, 1)
   // and dQ accumulator stay in L2; otherwise across heads. With one unit per CTA the key tiles run heavy-first.
   // With sinks (see SinkWork) a CTA takes one key tile, or a piece of one that holds sinks.
   const int n_bh = p.B * p.Hkv;
-  SinkWork sw;
+  SinkWork sw{};
   if constexpr (kSink) sw = sink_work(p, blockIdx.x);
   const int bh = kSink ? sw.bh : p.head_major ? blockIdx.x / p.n_grp : blockIdx.x % n_bh;
   const int grp = kSink ? sw.kblk : p.head_major ? blockIdx.x % p.n_grp : blockIdx.x / n_bh;

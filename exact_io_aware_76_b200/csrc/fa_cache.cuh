@@ -1,0 +1,1241 @@
+// fa_cache.cuh -- a paged e4m3 K/V cache on sm_100a: quantising new tokens into its pages, and attention over it.
+//
+// The cache: pages of `page` tokens, codes [num_pages, Hkv, page, D] (e4m3) and one fp32 scale per page and head for
+// K and for V (value = code * scale); a table [B, max_pages] of page numbers and a length per sequence. A page of one
+// head is contiguous (page * D bytes), so it arrives as one TMA box, and 128 keys of a head are 128 / page boxes.
+//
+// Attention without converting the cache. K and V stay e4m3 all the way into the tensor core (tcgen05 kind::f8f6f4);
+// it is the other operand that is brought to 8 bits, without loss: a 16-bit number has 8 (bf16) or 11 (fp16)
+// significant bits and an e4m3 number 4, so q = q1 + q2 (+ q3) with q1 = e4m3(q), q2 = e4m3(q - q1) and, for fp16,
+// q3 = e5m2(q - q1 - q2) (3 bits are left, and e5m2 reaches further down) is exact as long as the parts stay in range.
+// Each query row is first scaled by a power of two that brings its largest element to [128, 256); elements below
+// 2^-9 of the largest lose what falls under the last part's smallest step, an absolute error of at most 2^-17 (bf16) or
+// 2^-24 (fp16) of the row's largest element. S = q K^T is the sum of the parts' products in the fp32 accumulator.
+// The probabilities are split the same way (bf16 outputs: relative error 2^-8, as bf16 probabilities have; fp16:
+// 2^-11, set by their fp16 rounding before the split).
+//
+// Scales. With ks, vs the scales of key j's page and c = scale * log2 e, the weight that reaches the PV product is
+//   w_ij = 2^(s_ij c ks + log2 vs - m_i + 5),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
+// with m_i the running maximum of s c ks + log2 vs: the V scale is part of the exponent, so pages of any scales share one
+// accumulator, and the largest weights have full precision whatever the scales are. The factor 2^5 uses
+// e4m3's range upwards (m may lag by up to 3, so w <= 2^8) and leaves 2^-14 .. 2^-9 below for small weights.
+// Scales lie in [2^-50, 2^50], so l (at most 2^(5+3+100) times the number of keys) stays finite.
+//
+// Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
+// tiles, and before them the tiles with sinks). All units' tiles are laid end to end and every CTA takes an equal
+// run of them, whatever the lengths are, so a batch with one long sequence loads the SMs evenly. Units cut by a
+// run's border leave fp32 partial sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so
+// results repeat bit for bit.
+#pragma once
+#include "fa_fwd.cuh"
+
+namespace fa {
+
+constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that the workspace size needs no device
+constexpr float kCacheLag = 3.0f;    // how far the running maximum may lag (log2)
+constexpr float kCacheShift = 5.0f;  // weights carry 2^5 (see above)
+
+struct CacheParams {
+  const void* q;         // [B, Sq, H, D]
+  void* out;             // [B, Sq, H, D]
+  float* lse;            // [B, H, Sq]
+  const float* k_scale;  // [num_pages, Hkv]
+  const float* v_scale;
+  const int* table;      // [B, max_pages]
+  const int* lens;       // [B]
+  float* part_o;         // [kCacheCtas, 2, rows per unit, D]
+  float* part_ml;        // [kCacheCtas, 2, rows per unit, 2]
+  int4* cuts;            // [kCacheCtas] the unit cut at a CTA's first tile: item, K/V head, last CTA (item < 0: none)
+  int B, H, Hkv, group, Sq;
+  int n_rows, n_mt;      // query rows of a (sequence, K/V head) = Sq * group; units they make
+  int page, max_pages, num_pages;
+  int win_left, sinks;   // win_left < 0: no window (sinks = 0 then)
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------------------------------------------ append
+struct AppendParams {
+  const void *k, *v;     // new K and V, [B, T, Hkv, D]
+  uint8_t *k_pages, *v_pages;  // [num_pages, Hkv, page, D]
+  float *k_scale, *v_scale;    // [num_pages, Hkv]
+  const int* table;
+  const int* lens;       // lengths after the append
+  const int* counts;     // new tokens per sequence (null: T)
+  int B, T, Hkv, page, max_pages, num_pages;
+  int n_touch;           // pages that T tokens can touch
+};
+
+__device__ __forceinline__ uint32_t e4m3x2_from_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_from_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool kBF16>
+__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
+  if (kBF16) {
+    a = __uint_as_float(v << 16);
+    b = __uint_as_float(v & 0xffff0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    a = f.x;
+    b = f.y;
+  }
+}
+
+// The smallest power of two s with amax <= 448 s, exponent within [-50, 50] (448 = 0.875 * 2^9).
+__device__ __forceinline__ float append_scale(float amax) {
+  int e = 0;
+  const float m = frexpf(amax, &e);
+  e = amax > 0.f ? e - 9 + (m > 0.875f ? 1 : 0) : -50;
+  e = max(-50, min(50, e));
+  return __int_as_float((e + 127) << 23);
+}
+
+// One CTA per (sequence, page its new tokens touch, head, K or V): it alone writes that page of that head, so a
+// larger scale can move the page's earlier codes in place. Power-of-two scales make that move exact (but for codes that
+// become subnormal), and cost no precision: e4m3's steps are relative. Bound by bytes for long prompts (read 16 bits,
+// write 8), by latency for single tokens.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams p) {
+  constexpr int kVecs = D / 8;            // 8-element vectors per token
+  constexpr int kRows = 128 / kVecs;      // tokens per pass of the CTA
+  __shared__ float red[4];
+  long long i = blockIdx.x;
+  const int which = static_cast<int>(i & 1);
+  i >>= 1;
+  const int h = static_cast<int>(i % p.Hkv);
+  i /= p.Hkv;
+  const int touch = static_cast<int>(i % p.n_touch);
+  const int b = static_cast<int>(i / p.n_touch);
+  const int len = p.lens[b];
+  const int count = min(max(p.counts ? p.counts[b] : p.T, 0), min(p.T, max(len, 0)));
+  const int first = len - count;
+  const int n = first / p.page + touch;
+  if (count == 0 || n >= p.max_pages || static_cast<long long>(n) * p.page >= len) return;
+  const int pid = p.table[static_cast<size_t>(b) * p.max_pages + n];
+  if (pid < 0 || pid >= p.num_pages) return;
+  const int lo = max(first, n * p.page), hi = min(len, n * p.page + p.page);  // positions written here
+  const int vec = threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
+  const uint16_t* src = static_cast<const uint16_t*>(which ? p.v : p.k) +
+                        ((static_cast<size_t>(b) * p.T + (p.T - len + lo)) * p.Hkv + h) * D + vec * 8;
+  const size_t stride = static_cast<size_t>(p.Hkv) * D;
+  uint8_t* codes = (which ? p.v_pages : p.k_pages) + (static_cast<size_t>(pid) * p.Hkv + h) * p.page * D;
+  float* sc = (which ? p.v_scale : p.k_scale) + static_cast<size_t>(pid) * p.Hkv + h;
+
+  float amax = 0.f;  // over finite values
+  for (int r = r0; r < hi - lo; r += kRows) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + r * stride);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, c;
+      unpack2<kBF16>(w[e], a, c);
+      a = fabsf(a);
+      c = fabsf(c);
+      amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+      amax = fmaxf(amax, c < INFINITY ? c : 0.f);
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  const int kept = lo - n * p.page;  // earlier tokens of this page
+  const float old = kept > 0 ? *sc : 0.f;
+  __syncthreads();
+  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float now = fmaxf(append_scale(amax), old);
+  if (kept > 0 && now != old) {
+    const float f = old / now;
+    for (int t = threadIdx.x; t < kept * (D / 4); t += 128) {
+      uint32_t* c4 = reinterpret_cast<uint32_t*>(codes) + t;
+      const uint32_t c = *c4;
+      float x0, x1, x2, x3;
+      unpack2<false>(f16x2_from_e4m3x2(c & 0xffffu), x0, x1);
+      unpack2<false>(f16x2_from_e4m3x2(c >> 16), x2, x3);
+      *c4 = pack4_e4m3(x0 * f, x1 * f, x2 * f, x3 * f);
+    }
+  }
+  if (threadIdx.x == 0) *sc = now;
+  // A power of two (always, unless the caller's earlier scale was none) is divided by exactly as a product.
+  const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0u;
+  const float inv = 1.f / now;
+  for (int r = r0; r < hi - lo; r += kRows) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + r * stride);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      unpack2<kBF16>(w[e], x[2 * e], x[2 * e + 1]);
+      x[2 * e] = pow2 ? x[2 * e] * inv : x[2 * e] / now;
+      x[2 * e + 1] = pow2 ? x[2 * e + 1] * inv : x[2 * e + 1] / now;
+    }
+    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(kept + r) * D + vec * 8) =
+        make_uint2(pack4_e4m3(x[0], x[1], x[2], x[3]), pack4_e4m3(x[4], x[5], x[6], x[7]));
+  }
+}
+
+// ------------------------------------------------------------------------------------------------- work split
+// One item: a (sequence, block of kRows query rows); n: the tiles of its walk (at least one, so that rows without
+// a visible key are visited and written).
+struct CacheItem {
+  int b, row0, rows;    // query rows [row0, row0 + rows) of the Sq * group rows; row r: query r / group
+  int c0;               // aligned key of query 0 = length - Sq
+  int c_min, c_max;     // aligned keys of the first and last row
+  int key_lo, key_hi;   // keys its rows see: [key_lo, key_hi] and the sinks below key_lo
+  int j_lo, n_sink, n;  // first window tile, sink tiles before it, tiles in all
+};
+
+template <int kRows>
+__device__ __forceinline__ CacheItem cache_item(const CacheParams& p, int x) {
+  CacheItem t;
+  t.b = x / p.n_mt;
+  t.row0 = (x % p.n_mt) * kRows;
+  t.rows = min(kRows, p.n_rows - t.row0);
+  const int len = max(0, min(__ldg(p.lens + t.b), p.max_pages * p.page));
+  t.c0 = len - p.Sq;
+  t.c_min = t.c0 + t.row0 / p.group;
+  t.c_max = t.c0 + (t.row0 + t.rows - 1) / p.group;
+  t.key_hi = t.c_max;
+  t.key_lo = p.win_left >= 0 ? max(0, t.c_min - p.win_left) : 0;
+  t.j_lo = t.n_sink = 0;
+  t.n = 1;
+  if (t.key_hi >= 0) {
+    t.j_lo = t.key_lo / 128;
+    t.n_sink = min((p.sinks + 127) / 128, t.j_lo);
+    t.n = t.n_sink + t.key_hi / 128 - t.j_lo + 1;
+  }
+  return t;
+}
+__device__ __forceinline__ int cache_key0(const CacheItem& t, int w) {
+  return (w < t.n_sink ? w : t.j_lo + w - t.n_sink) * 128;
+}
+// Whether the tile at key0 holds keys that none of the item's rows sees (what the page holds there may be stale).
+__device__ __forceinline__ bool cache_ragged(const CacheParams& p, const CacheItem& t, int key0) {
+  return key0 + 127 > t.key_hi || (key0 < t.key_lo && key0 + 127 >= p.sinks);
+}
+
+// A position in the row of all tiles: tile w of (item x, K/V head hk). Order: items, then heads, then tiles.
+struct CachePos {
+  int x, hk, w;
+};
+template <int kRows>
+struct CacheWalk {
+  CachePos at;
+  CacheItem item;
+  __device__ __forceinline__ void start(const CacheParams& p, const CachePos& s) {
+    at = s;
+    item = cache_item<kRows>(p, at.x);
+  }
+  // Ahead by `by` tiles (the caller stays within the row of tiles).
+  __device__ __forceinline__ void advance(const CacheParams& p, int by) {
+    at.w += by;
+    while (at.w >= item.n) {
+      at.w -= item.n;
+      if (++at.hk == p.Hkv) {
+        at.hk = 0;
+        if (++at.x >= p.B * p.n_mt) return;
+        item = cache_item<kRows>(p, at.x);
+      }
+    }
+  }
+};
+
+struct CacheRun {
+  int count;     // tiles of this CTA
+  CachePos first;
+};
+
+// This CTA's run of tiles, found by every thread together (kThreads of them): all items' tiles are counted, then the
+// item holding the run's first tile is searched. Also notes the unit cut there, for the join.
+template <int kRows, int kThreads>
+__device__ __forceinline__ CacheRun cache_run(const CacheParams& p, long long* scratch /* kThreads / 32 + 1 */,
+                                              CacheRun* shared) {
+  const int items = p.B * p.n_mt, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  long long sum = 0;
+  for (int x = tid; x < items; x += kThreads) sum += cache_item<kRows>(p, x).n;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  if (lane == 0) scratch[warp] = sum;
+  if (tid == 0) shared->count = 0;
+  __syncthreads();
+  long long total = 0;
+  for (int i = 0; i < kWarps; ++i) total += scratch[i];
+  total *= p.Hkv;
+  const long long share = (total + kCacheCtas - 1) / kCacheCtas;
+  const long long begin = share * blockIdx.x, end = min(begin + share, total);
+  if (begin < end) {
+    long long base = 0;
+    for (int x0 = 0; x0 < items; x0 += kThreads) {
+      const int x = x0 + tid;
+      const int n = x < items ? cache_item<kRows>(p, x).n : 0;
+      const long long mine = static_cast<long long>(n) * p.Hkv;
+      long long incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += o;
+      }
+      __syncthreads();
+      if (lane == 31) scratch[warp] = incl;
+      __syncthreads();
+      long long before = base;
+      for (int i = 0; i < warp; ++i) before += scratch[i];
+      const long long lo = before + incl - mine, hi = before + incl;
+      if (lo <= begin && begin < hi) {
+        const long long rel = begin - lo;
+        CacheRun r;
+        r.count = static_cast<int>(end - begin);
+        r.first = {x, static_cast<int>(rel / n), static_cast<int>(rel % n)};
+        *shared = r;
+        // The unit holding the tile before: cut at `begin` if it goes on here; its first CTA's successor joins it.
+        int4 cut = make_int4(-1, 0, 0, 0);
+        const long long u0 = begin - r.first.w;
+        if (r.first.w > 0 && u0 / share == blockIdx.x - 1)
+          cut = make_int4(x, r.first.hk, static_cast<int>((u0 + n - 1) / share), 0);
+        p.cuts[blockIdx.x] = cut;
+      }
+      for (int i = 0; i < kWarps; ++i) base += scratch[i];
+      if (begin < base) break;
+    }
+  } else if (tid == 0) {
+    p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+  __syncthreads();
+  return *shared;
+}
+
+// Where a piece of a unit leaves its sums: slot 0 of its CTA if the unit began before, slot 1 if it goes on after.
+__device__ __forceinline__ int cache_slot(int cta, int w0) { return cta * 2 + (w0 > 0 ? 0 : 1); }
+
+// Joins the pieces of every cut unit: CTA c takes the unit whose second piece begins CTA c's run.
+template <int D, bool kBF16, int kRows>
+__global__ void __launch_bounds__(256) fa_cache_join_kernel(const CacheParams p) {
+  const int4 cut = p.cuts[blockIdx.x];
+  if (cut.x < 0) return;
+  const CacheItem t = cache_item<kRows>(p, cut.x);
+  const int c_first = blockIdx.x - 1, c_last = cut.z;
+  for (int e = threadIdx.x; e < t.rows * (D / 4); e += blockDim.x) {
+    const int r = e / (D / 4), d = e % (D / 4) * 4;
+    float m = -INFINITY;
+    for (int c = c_first; c <= c_last; ++c) {
+      const size_t s = static_cast<size_t>(cache_slot(c, c > c_first)) * kRows + r;
+      m = fmaxf(m, p.part_ml[s * 2]);
+    }
+    const float m_use = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c_first; c <= c_last; ++c) {
+      const size_t s = static_cast<size_t>(cache_slot(c, c > c_first)) * kRows + r;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + s * 2);
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m_use);
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + s * D + d);
+      l = fmaf(ml.y, f, l);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no visible key (a NaN stays one)
+    const int row = t.row0 + r, i = row / p.group, h = cut.y * p.group + row % p.group;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(t.b) * p.Sq + i) * p.H + h) * D + d;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack2<kBF16>(o.x * inv, o.y * inv), pack2<kBF16>(o.z * inv, o.w * inv));
+    if (d == 0)
+      p.lse[(static_cast<size_t>(t.b) * p.H + h) * p.Sq + i] =
+          l == 0.f ? -INFINITY : (m + log2f(l) - kCacheShift) * kLn2;
+  }
+}
+
+// --------------------------------------------------------------------------------------------- shared pieces
+constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A in e5m2 (B in e4m3)
+
+// kFew: at most 32 query rows per unit (decoding); else blocks of 256 rows (chunks of prompts).
+template <int D, bool kBF16, bool kFew>
+struct CacheSmem {
+  static constexpr int kParts = kBF16 ? 2 : 3;       // e4m3 parts of q and of the probabilities
+  static constexpr int kRows = kFew ? 32 : 256;
+  static constexpr int kNQ = kFew ? 1 : 2;           // 128-row Q tiles
+  static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
+  static constexpr int kStages = (kFew && kBF16) ? 5 : 4;
+  static constexpr int kQOff = 0;                    // [part][Q tile]
+  static constexpr int kKOff = kQOff + kParts * kNQ * kTile;
+  static constexpr int kVOff = kKOff + kStages * kTile;
+  static constexpr int kXOff = kVOff + kStages * kTile;  // kFew: the quarters' sums, 4 x 32 rows x 33 floats
+  static constexpr int kXBytes = kFew ? 4 * 32 * 33 * 4 : 0;
+  static constexpr int kFacOff = kXOff + kXBytes;    // per stage: k factor, log2 v scale, 1 / v scale of 8 key groups
+  static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per quarter [2][4][32]
+  static constexpr int kMlBytes = kFew ? (32 + 256) * 4 : 0;
+  static constexpr int kBarOff = kMlOff + kMlBytes;
+  static constexpr int kNumBars = 3 * kStages + 12;
+  static constexpr int kRunOff = kBarOff + kNumBars * 8;
+  static constexpr int kScanOff = kRunOff + 16;
+  static constexpr int kMiscOff = kScanOff + 13 * 8;
+  static constexpr int kAlloc = kMiscOff + 16 + 1024;
+  static constexpr int kThreads = kFew ? 256 : 384;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+// The TMA warp: walks the run's tiles, a lane per 16-key group, four tiles per batch. The page numbers of the batch
+// after next and the scales of the next batch are loaded while this batch's copies are issued, so that neither of the two
+// dependent loads is waited for. Pages that no row sees, and page numbers outside the cache, are copied from beyond the
+// tensor's end: the copy engine writes zeros and reads nothing.
+template <int kRows, int kStages>
+__device__ __forceinline__ void cache_producer(const CacheParams& p, const CacheRun& run, const CUtensorMap& tm_k,
+                                               const CUtensorMap& tm_v, uint8_t* smem_k, uint8_t* smem_v, float* fac,
+                                               uint64_t* k_full, uint64_t* v_full, uint64_t* kv_empty,
+                                               volatile int* abort_flag) {
+  const int lane = lane_id(), tt = lane >> 3, grp = lane & 7;
+  struct Slot {
+    int row;  // first row of the page in the [num_pages * Hkv * page, D] view, < 0: none
+    int hk, id;
+    float ks, vs;
+  };
+  CacheWalk<kRows> walk;
+  int ahead = tt;  // tile index (within the run) of the walk's position
+  if (ahead < run.count) {
+    walk.start(p, run.first);
+    walk.advance(p, tt);
+  }
+  auto load_id = [&]() {
+    Slot s;
+    s.id = -1;
+    s.hk = 0;
+    s.ks = s.vs = 0.f;
+    if (ahead < run.count) {
+      const CacheItem& t = walk.item;
+      const int key = cache_key0(t, walk.at.w) + grp * 16;
+      const int n = key / p.page, pk = n * p.page;
+      s.hk = walk.at.hk;
+      if (n < p.max_pages && pk <= t.key_hi && (pk + p.page > t.key_lo || pk < p.sinks))
+        s.id = __ldg(p.table + static_cast<size_t>(t.b) * p.max_pages + n);
+      ahead += 4;
+      if (ahead < run.count) walk.advance(p, 4);
+    }
+    return s;
+  };
+  auto load_scales = [&](Slot& s) {
+    s.row = -1;
+    if (s.id >= 0 && s.id < p.num_pages) {
+      const size_t i = static_cast<size_t>(s.id) * p.Hkv + s.hk;
+      s.ks = __ldg(p.k_scale + i);
+      s.vs = __ldg(p.v_scale + i);
+      s.row = static_cast<int>(i * p.page);
+    }
+  };
+  const int beyond = p.num_pages * p.Hkv * p.page;
+  const bool leads = (grp * 16) % p.page == 0;  // this lane's group starts a page
+  Slot cur = load_id();
+  load_scales(cur);
+  Slot nxt = load_id();
+  int g = 0;
+  bool ok = true;
+  for (int t0 = 0; ok && t0 < run.count; t0 += 4) {
+    Slot far = load_id();
+    load_scales(nxt);
+    for (int u = 0; u < 4 && t0 + u < run.count; ++u) {
+      g = t0 + u;
+      const int s = g % kStages;
+      const bool got = g < kStages || mbar_wait(&kv_empty[s], ((g / kStages) - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      if (tt == u) {
+        const bool valid = cur.row >= 0;
+        fac[s * 24 + grp] = valid ? cur.ks : 0.f;
+        fac[s * 24 + 8 + grp] = valid ? log2f(cur.vs) : -INFINITY;  // a key without a page has weight 0
+        fac[s * 24 + 16 + grp] = valid ? 1.f / cur.vs : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&k_full[s], 16384);
+        mbar_arrive_expect_tx(&v_full[s], 16384);
+      }
+      __syncwarp();
+      if (tt == u && leads) {
+        const int row = cur.row >= 0 ? cur.row : beyond;
+        tma_load_2d(smem_k + s * 16384 + grp * 2048, &tm_k, &k_full[s], 0, row);
+        tma_load_2d(smem_v + s * 16384 + grp * 2048, &tm_v, &v_full[s], 0, row);
+      }
+      __syncwarp();
+    }
+    cur = nxt;
+    nxt = far;
+  }
+  if (*abort_flag) {
+    // Let the copies already issued land before the CTA exits (bounded; own flag, not the CTA's).
+    const int issued = ok ? run.count : g;
+    for (int i = max(0, issued - kStages); i < issued; ++i) {
+      int drain = 0;
+      mbar_wait(&k_full[i % kStages], (i / kStages) & 1, &drain);
+      drain = 0;
+      mbar_wait(&v_full[i % kStages], (i / kStages) & 1, &drain);
+    }
+  }
+}
+
+// The cleaning warp: in a ragged tile, V rows that no query row sees are set to 0, because their weights are 0 but
+// a stale byte may be a NaN (0 * NaN). (K needs none of this: masked scores are replaced.)
+template <int kRows, int kStages>
+__device__ __forceinline__ void cache_cleaner(const CacheParams& p, const CacheRun& run, uint8_t* smem_v,
+                                              uint64_t* v_full, uint64_t* v_clean, volatile int* abort_flag) {
+  CacheWalk<kRows> walk;
+  if (run.count > 0) walk.start(p, run.first);
+  const int lane = lane_id();
+  for (int g = 0; g < run.count; ++g) {
+    const CacheItem& t = walk.item;
+    const int key0 = cache_key0(t, walk.at.w);
+    if (cache_ragged(p, t, key0)) {
+      const int s = g % kStages;
+      const bool got = mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) return;
+      for (int i = lane; i < 128 * 8; i += 32) {
+        const int key = key0 + i / 8;
+        if (key > t.key_hi || (key < t.key_lo && key >= p.sinks))
+          *reinterpret_cast<uint4*>(smem_v + s * 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(v_clean);
+    }
+    if (g + 1 < run.count) walk.advance(p, 1);
+  }
+}
+
+// 2^k as a float, k in [-126, 127].
+__device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) << 23); }
+
+// Row scaling of q: with amax the row's largest magnitude, q * mul has its largest element in [128, 256), and a
+// product with it is multiplied by back = 1 / mul. A row with an infinity or a NaN gets back = NaN, so that its scores are
+// NaN as they would be.
+__device__ __forceinline__ void q_row_scale(uint32_t amax_bits, float& mul, float& back) {
+  // (magnitudes of floats order as their bits; bits of 2^128 and above are infinities and NaNs)
+  int e = static_cast<int>(amax_bits >> 23) - 127;
+  e = max(e, -100);  // smaller rows keep a fixed factor (0 rows included)
+  mul = pow2i(min(7 - e, 127));
+  back = pow2i(max(e - 7, -126));
+  if (amax_bits >= 0x7f800000u) {
+    mul = 1.f;
+    back = __int_as_float(0x7fc00000);
+  }
+}
+
+// Eight elements of q (16 bytes) -> kParts x 8 e4m3 codes.
+template <bool kBF16, int kParts>
+__device__ __forceinline__ void q_split8(const uint4& v, float mul, uint2* part) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2<kBF16>(w[i], a, b);
+    h[i] = pack2_f16(a * mul, b * mul);  // at most 256, 11 significant bits: exact down to 2^-24
+  }
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = q < 2 ? e4m3x2_from_f16x2(h[i]) : e5m2x2_from_f16x2(h[i]);
+      if (q + 1 < kParts) h[i] = sub_f16x2(h[i], f16x2_from_e4m3x2(c[i]));
+    }
+    part[q] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+}
+template <bool kBF16>
+__device__ __forceinline__ uint32_t q_amax8(const uint4& v, uint32_t amax) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2<kBF16>(w[i], a, b);
+    amax = max(amax, max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+  }
+  return amax;
+}
+
+// Four weights -> their e4m3 parts, packed four to a register (first weight lowest).
+template <int kParts>
+__device__ __forceinline__ void p_split4(float a, float b, float c, float d, uint32_t* part) {
+  uint32_t h0 = pack2_f16(a, b), h1 = pack2_f16(c, d);
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    const uint32_t c0 = q < 2 ? e4m3x2_from_f16x2(h0) : e5m2x2_from_f16x2(h0);
+    const uint32_t c1 = q < 2 ? e4m3x2_from_f16x2(h1) : e5m2x2_from_f16x2(h1);
+    part[q] = c0 | (c1 << 16);
+    if (q + 1 < kParts) {
+      h0 = sub_f16x2(h0, f16x2_from_e4m3x2(c0));
+      h1 = sub_f16x2(h1, f16x2_from_e4m3x2(c1));
+    }
+  }
+}
+
+// -------------------------------------------------------------------------------- attention of few query rows
+// Decoding: up to 32 rows (the query heads of a K/V head, times a few tokens) against a long cache. The bytes of the cache
+// bound it, so everything else is arranged to hide behind the copies. An M = 128 product costs the same however few of
+// its rows are used, so the rows are put into the A operand four times, at lanes 0, 32, 64 and 96, and each warp
+// of the softmax warpgroup takes 32 of the tile's 128 keys for its copy: four warps share a tile's exponentials
+// without exchanging anything, each with its own running maximum, sum and rows of O (its P is 0 at the
+// other warps' keys). The four are joined once, at the end of the unit.
+//
+// Warps: 0-3 softmax, 4 TMA, 5 MMA, 6 cleaner (see cache_cleaner), 7 idle.
+// TMEM columns: S in two buffers [0,128) and [128,256), O [256,384), parts of P from 384, 32 columns each.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(256, 1)
+    fa_cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const CacheParams p) {
+  using L = CacheSmem<D, kBF16, true>;
+  constexpr int kStages = L::kStages, kParts = L::kParts, kRows = L::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* k_full = bars;
+  uint64_t* v_full = k_full + kStages;
+  uint64_t* kv_empty = v_full + kStages;
+  uint64_t* s_full = kv_empty + kStages;  // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = s_full + 3;
+  uint64_t* q_ready = s_full + 4;
+  uint64_t* v_clean = s_full + 5;
+  uint64_t* joint = s_full + 6;           // the four softmax warps among themselves
+  uint64_t* mma_done = s_full + 7;
+  float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
+  float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [32]
+  float* q_m = row_back + 32;                                     // [4][32]
+  float* q_l = q_m + 128;                                         // [4][32]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, 128);
+    mbar_init(o_full, 1);
+    mbar_init(q_ready, 128);
+    mbar_init(v_clean, 32);
+    mbar_init(joint, 128);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_holder, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
+                                                     reinterpret_cast<CacheRun*>(smem + L::kRunOff));
+  if (run.count > 0) {
+    if (warp == 4) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      cache_producer<kRows, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
+                                     kv_empty, abort_flag);
+    } else if (warp == 5 && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
+      constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
+      const uint32_t o_tmem = tmem + 256, p_tmem = tmem + 384;
+      auto issue_s = [&](int g) {
+        const uint64_t b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_ss_f8(tmem + (g & 1) * 128, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
+                       id_s | (q < 2 ? 0u : kE5M2A),
+                       (q > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&s_full[g & 1]);
+      };
+      CacheWalk<kRows> walk;
+      walk.start(p, run.first);
+      int cleaned = 0;
+      bool ok = true;
+      for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
+        const int left = min(run.count - g, walk.item.n - walk.at.w);  // tiles of this unit in the run
+        ok = mbar_wait(q_ready, unit & 1, abort_flag) &&
+             mbar_wait(&k_full[g % kStages], (g / kStages) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after_sync();
+        issue_s(g);
+        for (int it = 0; it < left; ++it, ++g) {
+          const int s = g % kStages;
+          if (it + 1 < left) {
+            // The other S buffer was read before the previous tile's weights were published.
+            if (!mbar_wait(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after_sync();
+            issue_s(g + 1);
+          }
+          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+          if (cache_ragged(p, walk.item, cache_key0(walk.item, walk.at.w + it))) {
+            if (!mbar_wait(v_clean, cleaned & 1, abort_flag)) { ok = false; break; }
+            ++cleaned;
+          }
+          if (!mbar_wait(p_full, g & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts_f8(o_tmem, p_tmem + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
+                         id_o | (q < 2 ? 0u : kE5M2A),
+                         (it > 0 || q > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(o_full);
+          umma_commit(&kv_empty[s]);
+        }
+        if (ok && g < run.count) walk.advance(p, left);
+      }
+      umma_commit(mma_done);
+      int drain = 0;
+      mbar_wait(mma_done, 0, &drain);
+    } else if (warp == 6) {
+      cache_cleaner<kRows, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
+    } else if (warp < 4) {
+      // ---------------------------------------------------------------- softmax
+      const uint32_t lane_base = tmem + ((warp * 32) << 16);
+      const uint32_t o_tmem = lane_base + 256, p_tmem = lane_base + 384;
+      {
+        // This warp's rows of P are 0 but at its own keys (columns 8 * warp .. + 7 of each part).
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) tmem_st_x32(p_tmem + q * 32, z);
+        tmem_st_wait();
+      }
+      int joins = 0;
+      auto join = [&]() {  // all 128 threads of these warps, bounded like every wait
+        mbar_arrive(joint);
+        return mbar_wait(joint, joins++ & 1, abort_flag);
+      };
+      CacheWalk<kRows> walk;
+      walk.start(p, run.first);
+      bool ok = true;
+      for (int g = 0; ok && g < run.count;) {
+        const CacheItem t = walk.item;
+        const int hk = walk.at.hk, w0 = walk.at.w;
+        const int left = min(run.count - g, t.n - w0);
+        // ---- q: four threads per row; each row goes to its four places in the A operand
+        {
+          const int r = threadIdx.x >> 2, piece = threadIdx.x & 3;
+          constexpr int kVec = D / 32;  // 16-byte pieces of 8 elements per thread
+          uint4 v[kVec];
+          uint32_t amax = 0;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < t.rows) {
+            const int row = t.row0 + r, qi = row / p.group, h = hk * p.group + row % p.group;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(p.q) + ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D) + piece * kVec;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[i] = src[i];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
+          }
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          float mul, back;
+          q_row_scale(amax, mul, back);
+          if (piece == 0) row_back[r] = back * p.scale_log2;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            uint2 part[kParts];
+            q_split8<kBF16, kParts>(v[i], mul, part);
+            const int e8 = piece * kVec + i;  // 8-byte unit of the row
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int m = c * 32 + r;
+              uint8_t* dst = smem + L::kQOff + m * 128 + ((e8 >> 1) ^ (m & 7)) * 16 + (e8 & 1) * 8;
+#pragma unroll
+              for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q];
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(q_ready);
+          if (!join()) { ok = false; break; }
+        }
+        const float c_row = row_back[lane];
+        const int row = t.row0 + min(static_cast<int>(lane), t.rows - 1);
+        const int aligned = t.c0 + row / p.group;
+        const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
+        float m = -INFINITY, l = 0.f;
+        for (int it = 0; it < left; ++it, ++g) {
+          const int s = g % kStages;
+          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * warp;
+          if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag) ||
+              !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after_sync();
+          float x[32];
+          tmem_ld_x32(lane_base + (g & 1) * 128 + 32 * warp, reinterpret_cast<uint32_t*>(x));
+          const float* f = fac + s * 24 + 2 * warp;
+          const float a0 = c_row * f[0], a1 = c_row * f[1], lv0 = f[8], lv1 = f[9], iv0 = f[16], iv1 = f[17];
+          const bool masked = tile0 + 127 > t.c_min ||
+                              (p.win_left >= 0 && tile0 < t.c_max - p.win_left && tile0 + 127 >= p.sinks);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            x[c] = fmaf(x[c], c < 16 ? a0 : a1, c < 16 ? lv0 : lv1);
+            if (masked && (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks))) x[c] = -INFINITY;
+            mx = fmaxf(mx, x[c]);
+          }
+          const float m_new = fmaxf(m, mx);
+          // The previous tile's product has to be done with P and O.
+          if (it > 0 && !mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after_sync();
+          if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
+            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+            if (it > 0) {
+#pragma unroll
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                float o[32];
+                tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+              }
+            }
+            l *= alpha;
+            m = m_new;
+          }
+          const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
+          float sum0 = 0.f, sum1 = 0.f;
+          uint32_t pk[kParts][8];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[c + e] + off);
+            (c < 16 ? sum0 : sum1) += (w[0] + w[1]) + (w[2] + w[3]);
+            uint32_t part[kParts];
+            p_split4<kParts>(w[0], w[1], w[2], w[3], part);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) pk[q][c / 4] = part[q];
+          }
+          l += sum0 * iv0 + sum1 * iv1;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) tmem_st_x8(p_tmem + q * 32 + 8 * warp, pk[q]);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(p_full);
+        }
+        if (!ok) break;
+        // ---- the unit's (or piece's) end: join the four quarters
+        q_m[warp * 32 + lane] = m;
+        q_l[warp * 32 + lane] = l;
+        if (!join()) { ok = false; break; }
+        float m_all = -INFINITY, l_all = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m_all = fmaxf(m_all, q_m[q * 32 + lane]);
+        const float m_use = m_all == -INFINITY ? 0.f : m_all;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) l_all += q_l[q * 32 + lane] * ex2_approx(q_m[q * 32 + lane] - m_use);
+        const bool whole = left == t.n;
+        float f = ex2_approx(m - m_use);
+        if (whole) f *= l_all == 0.f ? 0.f : 1.f / l_all;  // l = 0: no visible key (a NaN stays one)
+        const size_t slot = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * kRows;
+        if (warp == 0 && static_cast<int>(lane) < t.rows) {
+          if (whole) {
+            const int h = hk * p.group + row % p.group, qi = row / p.group;
+            p.lse[(static_cast<size_t>(t.b) * p.H + h) * p.Sq + qi] =
+                l_all == 0.f ? -INFINITY : (m_all + log2f(l_all) - kCacheShift) * kLn2;
+          } else {
+            *reinterpret_cast<float2*>(p.part_ml + (slot + lane) * 2) = make_float2(m_all, l_all);
+          }
+        }
+        if (!mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after_sync();
+        float* xo = reinterpret_cast<float*>(smem + L::kXOff);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+          // (a quarter that saw no key of this row has f = 0, and weights 0: its O is 0)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) xo[(warp * 32 + lane) * 33 + c] = o[c] * f;
+          if (!join()) { ok = false; break; }
+          for (int r = warp; r < t.rows; r += 4) {
+            const float v = (xo[r * 33 + lane] + xo[(32 + r) * 33 + lane]) +
+                            (xo[(64 + r) * 33 + lane] + xo[(96 + r) * 33 + lane]);
+            if (whole) {
+              const int rr = t.row0 + r, qi = rr / p.group, h = hk * p.group + rr % p.group;
+              static_cast<uint16_t*>(p.out)[((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + c0 + lane] =
+                  static_cast<uint16_t>(pack2<kBF16>(v, 0.f));
+            } else {
+              p.part_o[(slot + r) * D + c0 + lane] = v;
+            }
+          }
+          if (!join()) { ok = false; break; }
+        }
+        if (!ok) break;
+        if (g < run.count) walk.advance(p, left);
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------- attention of many query rows
+// Chunks of prompts: units of 256 rows (two 128-row Q tiles, each with its own softmax warpgroup, thread = row), as in
+// the forward of fa_fwd.cuh: while one warpgroup runs the softmax of its tile the tensor core works on the other.
+// Bound by the tensor core (2 or 3 e4m3 products for each of S and O) and the exponentials.
+//
+// Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8 TMA, 9 MMA, 10 cleaner, 11 idle. TMEM columns: S0 [0,128),
+// S1 [128,256), O0 [256,384), O1 [384,512); the parts of P_t overwrite S_t, 32 columns each.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(384, 1)
+    fa_cache_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const CacheParams p) {
+  using L = CacheSmem<D, kBF16, false>;
+  constexpr int kStages = L::kStages, kParts = L::kParts, kRows = L::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* k_full = bars;
+  uint64_t* v_full = k_full + kStages;
+  uint64_t* kv_empty = v_full + kStages;
+  uint64_t* s_full = kv_empty + kStages;  // [2]
+  uint64_t* p_half = s_full + 2;          // [2] weights of keys 0..63 published
+  uint64_t* p_full = s_full + 4;          // [2]
+  uint64_t* o_full = s_full + 6;          // [2]
+  uint64_t* q_ready = s_full + 8;         // [2]
+  uint64_t* v_clean = s_full + 10;
+  uint64_t* mma_done = s_full + 11;
+  float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_half[t], 128);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&o_full[t], 1);
+      mbar_init(&q_ready[t], 128);
+    }
+    mbar_init(v_clean, 32);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
+                                                     reinterpret_cast<CacheRun*>(smem + L::kRunOff));
+  if (warp >= 8) {
+    regs_dec<88>();
+    if (run.count == 0) {
+    } else if (warp == 8) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      cache_producer<kRows, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
+                                     kv_empty, abort_flag);
+    } else if (warp == 9 && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
+      constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
+      auto issue_s = [&](int t, int g) {
+        const uint64_t a0 = sdesc_add(q_desc, t * L::kTile), b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_ss_f8(tmem + t * 128, sdesc_add(a0, q * 2 * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
+                       id_s | (q < 2 ? 0u : kE5M2A),
+                       (q > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&s_full[t]);
+      };
+      auto issue_o = [&](int t, int g, bool acc, int half) {
+        const uint64_t b0 = sdesc_add(v_desc, (g % kStages) * L::kTile);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
+            umma_ts_f8(tmem + 256 + t * 128, tmem + t * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
+                         id_o | (q < 2 ? 0u : kE5M2A),
+                       (acc || q > 0 || kk > 0) ? 1u : 0u);
+      };
+      CacheWalk<kRows> walk;
+      walk.start(p, run.first);
+      int cleaned = 0;
+      int steps[2] = {0, 0}, units[2] = {0, 0};  // tiles and units each Q tile has taken part in
+      bool ok = true;
+      for (int g = 0; ok && g < run.count;) {
+        const int left = min(run.count - g, walk.item.n - walk.at.w);  // tiles of this unit in the run
+        const int nq = walk.item.rows > 128 ? 2 : 1;                   // Q tiles with rows
+        ok = mbar_wait(&k_full[g % kStages], (g / kStages) & 1, abort_flag);
+        for (int t = 0; ok && t < nq; ++t) {
+          ok = mbar_wait(&q_ready[t], units[t]++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue_s(t, g);
+        }
+        for (int it = 0; ok && it < left; ++it, ++g) {
+          const int s = g % kStages;
+          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+          if (cache_ragged(p, walk.item, cache_key0(walk.item, walk.at.w + it))) {
+            if (!mbar_wait(v_clean, cleaned & 1, abort_flag)) { ok = false; break; }
+            ++cleaned;
+          }
+          bool next_k = false;
+          for (int t = 0; t < nq; ++t) {
+            const int u = steps[t]++;
+            if (!mbar_wait(&p_half[t], u & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after_sync();
+            issue_o(t, g, it > 0, 0);
+            if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after_sync();
+            issue_o(t, g, true, 1);
+            umma_commit(&o_full[t]);
+            if (it + 1 < left) {
+              if (!next_k) {
+                if (!mbar_wait(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after_sync();
+                next_k = true;
+              }
+              issue_s(t, g + 1);
+            }
+          }
+          umma_commit(&kv_empty[s]);
+        }
+        if (ok && g < run.count) walk.advance(p, left);
+      }
+      umma_commit(mma_done);
+      int drain = 0;
+      mbar_wait(mma_done, 0, &drain);
+    } else if (warp == 10) {
+      cache_cleaner<kRows, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
+    }
+  } else {
+    regs_inc<208>();
+    // ------------------------------------------------------------------ softmax warpgroups (thread = row)
+    const int t = warp / 4;
+    const uint32_t quarter = warp % 4;
+    const int r_tile = quarter * 32 + lane;  // row within the Q tile = TMEM lane
+    const uint32_t lane_base = tmem + ((quarter * 32) << 16);
+    const uint32_t s_tmem = lane_base + t * 128, o_tmem = lane_base + 256 + t * 128;
+    CacheWalk<kRows> walk;
+    if (run.count > 0) walk.start(p, run.first);
+    bool ok = true;
+    int step = 0;  // tiles this Q tile has taken part in
+    for (int g = 0; ok && g < run.count;) {
+      const CacheItem item = walk.item;
+      const int hk = walk.at.hk, w0 = walk.at.w;
+      const int left = min(run.count - g, item.n - w0);
+      if (item.rows <= t * 128) {  // no rows in this Q tile
+        g += left;
+        if (g < run.count) walk.advance(p, left);
+        continue;
+      }
+      const int r = t * 128 + r_tile;
+      const bool valid = r < item.rows;
+      const int row = item.row0 + min(r, item.rows - 1), qi = row / p.group, h = hk * p.group + row % p.group;
+      // ---- q: this thread's row into the A operand (its previous unit's products are complete: the warpgroup has
+      // seen their results)
+      float c_row;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + ((static_cast<size_t>(item.b) * p.Sq + qi) * p.H + h) * D);
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) amax = q_amax8<kBF16>(src[i], amax);
+        float mul, back;
+        q_row_scale(amax, mul, back);
+        c_row = back * p.scale_log2;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint2 part[kParts];
+          q_split8<kBF16, kParts>(src[i], mul, part);
+          uint8_t* dst = smem + L::kQOff + t * L::kTile + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kTile) = part[q];
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_ready[t]);
+      }
+      const int aligned = item.c0 + qi;
+      const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int it = 0; it < left; ++it, ++g, ++step) {
+        const int s = g % kStages;
+        if (!mbar_wait(&s_full[t], step & 1, abort_flag) ||
+            !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+        if (it > 0 && !mbar_wait(&o_full[t], (step - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after_sync();
+        float x[128];
+        tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(x));
+        const float* f = fac + s * 24;
+        const int key0 = cache_key0(item, w0 + it);
+        // x = s c ks + log2 vs, the weight's exponent
+#pragma unroll
+        for (int gr = 0; gr < 8; ++gr) {
+          const float a = c_row * f[gr], lv = f[8 + gr];
+          const uint64_t a2 = f2_pack(a, a), lv2 = f2_pack(lv, lv);
+#pragma unroll
+          for (int c = 16 * gr; c < 16 * gr + 16; c += 2) f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), a2, lv2), x[c], x[c + 1]);
+        }
+        if (key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks)) x[c] = -INFINITY;
+        }
+        float mq[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+          mq[0] = fmax3(mq[0], x[c], x[c + 1]);
+          mq[1] = fmax3(mq[1], x[c + 2], x[c + 3]);
+          mq[2] = fmax3(mq[2], x[c + 4], x[c + 5]);
+          mq[3] = fmax3(mq[3], x[c + 6], x[c + 7]);
+        }
+        const float mx = fmaxf(fmax3(mq[0], mq[1], x[124]), fmax3(mq[2], mq[3], fmax3(x[125], x[126], x[127])));
+        const float m_new = fmaxf(m, mx);
+        if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
+          const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+          if (it > 0) {
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[32];
+              tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= alpha;
+              tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+            }
+            tmem_st_wait();
+          }
+          l *= alpha;
+          m = m_new;
+        }
+        const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
+        const uint64_t off2 = f2_pack(off, off);
+        float lsum = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[kParts][16];
+#pragma unroll
+          for (int gr = 4 * half; gr < 4 * half + 4; ++gr) {
+            uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int c = 16 * gr; c < 16 * gr + 16; c += 4) {
+              float w0_, w1_, w2_, w3_;
+              f2_unpack(f2_add(f2_pack(x[c], x[c + 1]), off2), w0_, w1_);
+              f2_unpack(f2_add(f2_pack(x[c + 2], x[c + 3]), off2), w2_, w3_);
+              w0_ = ex2_approx(w0_);
+              w1_ = ex2_approx(w1_);
+              w2_ = ex2_approx(w2_);
+              w3_ = ex2_approx(w3_);
+              sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
+              uint32_t part[kParts];
+              p_split4<kParts>(w0_, w1_, w2_, w3_, part);
+#pragma unroll
+              for (int q = 0; q < kParts; ++q) pk[q][(c - 64 * half) / 4] = part[q];
+            }
+            float s0, s1;
+            f2_unpack(sum2, s0, s1);
+            lsum = fmaf(s0 + s1, f[16 + gr], lsum);
+          }
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) tmem_st_x16(s_tmem + q * 32 + half * 16, pk[q]);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(half ? &p_full[t] : &p_half[t]);
+        }
+        l += lsum;
+      }
+      if (!ok) break;
+      // ---- the unit's (or piece's) end
+      if (!mbar_wait(&o_full[t], (step - 1) & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after_sync();
+      const bool whole = left == item.n;
+      const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
+      const size_t slot = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * kRows + r;
+      uint16_t* orow = static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(item.b) * p.Sq + qi) * p.H + h) * D;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float o[32];
+        tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+        if (valid && whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) w[c / 2] = pack2<kBF16>(o[c] * inv, o[c + 1] * inv);
+          uint4* dst = reinterpret_cast<uint4*>(orow + c0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+        } else if (valid) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + c0);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(o[4 * v] * inv, o[4 * v + 1] * inv, o[4 * v + 2] * inv, o[4 * v + 3] * inv);
+        }
+      }
+      if (valid) {
+        if (whole)
+          p.lse[(static_cast<size_t>(item.b) * p.H + h) * p.Sq + qi] =
+              l == 0.f ? -INFINITY : (m + log2f(l) - kCacheShift) * kLn2;
+        else
+          *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m, l);
+      }
+      tc_fence_before_sync();
+      if (g < run.count) walk.advance(p, left);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -6,7 +6,7 @@ its operands spelled out one by one.
 
   tmem_ld_xN(taddr, r)          N columns into r[0..N), then tcgen05.wait::ld (N = 16, 32, 64, 128)
   tmem_ld_xN_pair(a1, r1, a2, r2)  two N-column loads and one wait (N = 32, 64)
-  tmem_st_xN(taddr, r)          N columns from r[0..N) (N = 16, 32, 64); the caller waits (tmem_st_wait)
+  tmem_st_xN(taddr, r)          N columns from r[0..N) (N = 8, 16, 32, 64); the caller waits (tmem_st_wait)
 """
 import os
 
@@ -50,7 +50,7 @@ def generate():
     out = ["// tmem_ldst.inc -- written by gen_tmem_ldst.py (do not edit by hand): tcgen05.ld (with its wait) and",
            "// tcgen05.st wrappers, shape 32x32b (lane = thread, one 32-bit column per register).", ""]
     out += [ld(n) for n in (16, 32, 64, 128)]
-    out += [st(n) for n in (16, 32, 64)]
+    out += [st(n) for n in (8, 16, 32, 64)]
     out += ["// Two loads (e.g. the S^T and dP^T rows of one thread) and a single wait.", ld_pair(32), ld_pair(64)]
     return "\n".join(out)
 

@@ -222,6 +222,51 @@ FA_API int fa_bwd_noalloc(const void* q, const void* k, const void* v, const voi
                           const void* dout, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int D,
                           int causal, float scale, int dtype, cudaStream_t stream);
 
+/*
+ * A paged K/V cache in 8 bits (beyond the pages). K and V of a token are e4m3 codes in pages of `page` tokens (16, 32, 64
+ * or 128), with one fp32 scale per page and head; a value is its code times its page's scale:
+ *   k_pages, v_pages [num_pages, Hkv, page, D] e4m3, 16-byte aligned;  k_scale, v_scale [num_pages, Hkv] fp32.
+ *   table [B, max_pages] int32: token t of sequence b is slot t % page of page table[b][t / page]. Entries need to be
+ *     valid only where tokens are written or seen; a number outside [0, num_pages) stands for no page.
+ *   lens [B] int32: tokens of each sequence, those of this call included; at most max_pages * page count.
+ * All of it is device memory, read when the kernels run: a captured call replays with the lengths and pages of then.
+ *
+ * Append: rounds new tokens to e4m3 and writes them. k, v [B, T, Hkv, D] (dtype FA_F16 or FA_BF16); counts [B] int32 or
+ * NULL (T each): the last counts[b] of sequence b's T tokens are its newest, at positions lens[b] - counts[b] ..
+ * lens[b] - 1 (rows before them are padding and not read; counts are clamped to 0 .. min(T, lens[b])).
+ *   - A page's scale is the smallest power of two, within 2^-50 .. 2^50, that brings the largest finite magnitude of
+ *     its tokens to at most 448. A page that holds earlier tokens keeps the larger of its scale and the new tokens';
+ *     where that grows, its codes move to it (exact but for codes that become subnormal). A page's first token
+ *     starts a new scale, whatever the page held before.
+ *   - Rounding is to nearest even; infinities become +-448 times the scale, NaNs stay NaNs.
+ *   - Tokens without a page are dropped. Slots behind the last token are left as they were. No two sequences of a
+ *     call may append to the same page.
+ */
+FA_API int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                           const int* table, const int* lens, const int* counts, int B, int T, int Hkv, int D,
+                           int num_pages, int page, int max_pages, int dtype, cudaStream_t stream);
+
+/* Bytes of device workspace fa_cache_fwd needs (0 on invalid sizes): partial sums of at most two units per SM. */
+FA_API size_t fa_cache_workspace_size(int B, int Sq, int H, int Hkv, int D);
+
+/*
+ * Attention over the cache: q [B, Sq, H, D] are the queries of each sequence's last Sq tokens (their keys are in the
+ * cache already); out [B, Sq, H, D] and lse [B, H, Sq] as in fa_fwd_ex. With c = lens[b] - Sq + i, query i sees key j iff
+ * j <= c and (window_left < 0 or j >= c - window_left or j < sinks) and token j has a page. A row that sees no key
+ * (c < 0: the sequence is shorter than Sq) gets O = 0 and LSE = -inf.
+ *   - Scales must lie in 2^-50 .. 2^50 (any fp32 value there, a power of two or not).
+ *   - What stands in slots behind a sequence's end, or in tokens that none of the call's queries sees, does not matter (NaNs
+ *     included). A non-finite V that some query of the call sees may reach the call's other rows of that K/V head.
+ *   - Probabilities reach the PV product with the precision of the output type (relative error 2^-8 or 2^-11); q as it
+ *     is, but for elements below 2^-9 of their row's largest (absolute error 2^-17 of that).
+ *   - workspace: fa_cache_workspace_size bytes, 256-byte aligned; contents on entry do not matter. Results repeat
+ *     bit for bit.
+ */
+FA_API int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                        const float* v_scale, const int* table, const int* lens, void* out, float* lse, int B, int Sq,
+                        int H, int Hkv, int D, int num_pages, int page, int max_pages, int window_left, int sinks,
+                        float scale, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Static English description of a status code (never NULL). */
 FA_API const char* fa_status_string(int status);
 
