@@ -382,7 +382,7 @@ struct CacheSmem {
   static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per quarter [2][4][32]
   static constexpr int kMlBytes = kFew ? (32 + 256) * 4 : 0;
   static constexpr int kBarOff = kMlOff + kMlBytes;
-  static constexpr int kNumBars = 3 * kStages + 12;
+  static constexpr int kNumBars = 4 * kStages + 11;
   static constexpr int kRunOff = kBarOff + kNumBars * 8;
   static constexpr int kScanOff = kRunOff + 16;
   static constexpr int kMiscOff = kScanOff + 13 * 8;
@@ -491,8 +491,10 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
   }
 }
 
-// The cleaning warp: in a ragged tile, V rows that no query row sees are set to 0, because their weights are 0 but
-// a stale byte may be a NaN (0 * NaN). (K needs none of this: masked scores are replaced.)
+// The cleaning warp: hands every V tile on to the MMA thread, and in a ragged one first sets the V rows that no query
+// row sees to 0, because their weights are 0 but a stale byte may be a NaN (0 * NaN). (K needs none of this: masked
+// scores are replaced.) Every tile goes through here, ragged or not: a warp that waited for some tiles only could
+// be two phases of a stage's barrier ahead or behind and mistake one phase for another.
 template <int kRows, int kStages>
 __device__ __forceinline__ void cache_cleaner(const CacheParams& p, const CacheRun& run, uint8_t* smem_v,
                                               uint64_t* v_full, uint64_t* v_clean, volatile int* abort_flag) {
@@ -501,19 +503,19 @@ __device__ __forceinline__ void cache_cleaner(const CacheParams& p, const CacheR
   const int lane = lane_id();
   for (int g = 0; g < run.count; ++g) {
     const CacheItem& t = walk.item;
-    const int key0 = cache_key0(t, walk.at.w);
+    const int key0 = cache_key0(t, walk.at.w), s = g % kStages;
+    const bool got = mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag);
+    if (!__all_sync(0xffffffffu, got)) return;
     if (cache_ragged(p, t, key0)) {
-      const int s = g % kStages;
-      const bool got = mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) return;
       for (int i = lane; i < 128 * 8; i += 32) {
         const int key = key0 + i / 8;
         if (key > t.key_hi || (key < t.key_lo && key >= p.sinks))
           *reinterpret_cast<uint4*>(smem_v + s * 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
-      mbar_arrive(v_clean);
+      __syncwarp();
     }
+    if (lane == 0) mbar_arrive(&v_clean[s]);
     if (g + 1 < run.count) walk.advance(p, 1);
   }
 }
@@ -608,13 +610,13 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* k_full = bars;
   uint64_t* v_full = k_full + kStages;
   uint64_t* kv_empty = v_full + kStages;
-  uint64_t* s_full = kv_empty + kStages;  // [2]
+  uint64_t* v_clean = kv_empty + kStages;
+  uint64_t* s_full = v_clean + kStages;   // [2]
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = s_full + 3;
   uint64_t* q_ready = s_full + 4;
-  uint64_t* v_clean = s_full + 5;
-  uint64_t* joint = s_full + 6;           // the four softmax warps among themselves
-  uint64_t* mma_done = s_full + 7;
+  uint64_t* joint = s_full + 5;           // the four softmax warps among themselves
+  uint64_t* mma_done = s_full + 6;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [32]
   float* q_m = row_back + 32;                                     // [4][32]
@@ -628,13 +630,13 @@ __global__ void __launch_bounds__(256, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&kv_empty[s], 1);
+      mbar_init(&v_clean[s], 1);
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(p_full, 128);
     mbar_init(o_full, 1);
     mbar_init(q_ready, 128);
-    mbar_init(v_clean, 32);
     mbar_init(joint, 128);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -679,7 +681,6 @@ __global__ void __launch_bounds__(256, 1)
       };
       CacheWalk<kRows> walk;
       walk.start(p, run.first);
-      int cleaned = 0;
       bool ok = true;
       for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
         const int left = min(run.count - g, walk.item.n - walk.at.w);  // tiles of this unit in the run
@@ -696,11 +697,7 @@ __global__ void __launch_bounds__(256, 1)
             tc_fence_after_sync();
             issue_s(g + 1);
           }
-          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
-          if (cache_ragged(p, walk.item, cache_key0(walk.item, walk.at.w + it))) {
-            if (!mbar_wait(v_clean, cleaned & 1, abort_flag)) { ok = false; break; }
-            ++cleaned;
-          }
+          if (!mbar_wait(&v_clean[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
           if (!mbar_wait(p_full, g & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
           const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
@@ -929,13 +926,13 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* k_full = bars;
   uint64_t* v_full = k_full + kStages;
   uint64_t* kv_empty = v_full + kStages;
-  uint64_t* s_full = kv_empty + kStages;  // [2]
+  uint64_t* v_clean = kv_empty + kStages;
+  uint64_t* s_full = v_clean + kStages;   // [2]
   uint64_t* p_half = s_full + 2;          // [2] weights of keys 0..63 published
   uint64_t* p_full = s_full + 4;          // [2]
   uint64_t* o_full = s_full + 6;          // [2]
   uint64_t* q_ready = s_full + 8;         // [2]
-  uint64_t* v_clean = s_full + 10;
-  uint64_t* mma_done = s_full + 11;
+  uint64_t* mma_done = s_full + 10;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -946,6 +943,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&kv_empty[s], 1);
+      mbar_init(&v_clean[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -954,7 +952,6 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&o_full[t], 1);
       mbar_init(&q_ready[t], 128);
     }
-    mbar_init(v_clean, 32);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -1009,7 +1006,6 @@ __global__ void __launch_bounds__(384, 1)
       };
       CacheWalk<kRows> walk;
       walk.start(p, run.first);
-      int cleaned = 0;
       int steps[2] = {0, 0}, units[2] = {0, 0};  // tiles and units each Q tile has taken part in
       bool ok = true;
       for (int g = 0; ok && g < run.count;) {
@@ -1024,11 +1020,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int it = 0; ok && it < left; ++it, ++g) {
           const int s = g % kStages;
-          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
-          if (cache_ragged(p, walk.item, cache_key0(walk.item, walk.at.w + it))) {
-            if (!mbar_wait(v_clean, cleaned & 1, abort_flag)) { ok = false; break; }
-            ++cleaned;
-          }
+          if (!mbar_wait(&v_clean[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
           bool next_k = false;
           for (int t = 0; t < nq; ++t) {
             const int u = steps[t]++;

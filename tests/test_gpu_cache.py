@@ -107,6 +107,9 @@ CASES = [
     (8, 2, 1, 128, 16, [3000, 90, 1500], 255, 20, "f16"),
     (4, 1, 8, 64, 32, [3000, 4], 64, 200, "bf16"),             # sinks in two tiles
     (4, 4, 1, 128, 64, [900], 0, 1, "bf16"),                   # itself and the first token
+    (8, 8, 1, 128, 64, [100 + 331 * i for i in range(24)], -1, 0, "bf16"),  # many tiles and units per CTA
+    (8, 8, 1, 64, 16, [100 + 97 * i for i in range(40)], 700, 4, "f16"),
+    (4, 4, 70, 128, 32, [40 + 211 * i for i in range(24)], -1, 0, "bf16"),
     (33, 1, 1, 128, 64, [500, 129], -1, 0, "bf16"),            # one row too many for the small kernel
     (8, 2, 40, 64, 16, [300, 40, 17, 0], -1, 0, "f16"),
     (8, 2, 300, 128, 64, [300, 1000, 301], -1, 0, "bf16"),     # a whole prompt, and chunks of two
