@@ -638,7 +638,8 @@ int encode_pages_map(CUtensorMap* m, const void* base, int num_pages, int Hkv, i
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-constexpr int kFewRows = 32, kManyRows = 256;
+// Query rows per unit: the smallest block that holds a K/V head's rows of a sequence, or blocks of 256.
+int cache_rows(int n_rows) { return n_rows <= 8 ? 8 : n_rows <= 16 ? 16 : n_rows <= 32 ? 32 : 256; }
 struct CacheLayout {
   size_t ml, cuts, total;
 };
@@ -659,34 +660,35 @@ int check_cache_queries(int B, int Sq, int H, int Hkv, int D) {
   return FA_OK;
 }
 
-template <int D, bool BF16, bool FEW>
+template <int D, bool BF16, int R>
 int launch_cache(const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams& p, bool join, int dev,
                  cudaStream_t stream) {
-  using L = fa::CacheSmem<D, BF16, FEW>;
+  using L = fa::CacheSmem<D, BF16, R>;
   static bool attr_done[kMaxDevices] = {};
-  if constexpr (FEW) {
-    auto kern = fa::fa_cache_few_kernel<D, BF16>;
+  auto run = [&](auto kern) -> int {
     int rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done);
     if (rc) return rc;
     kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
-  } else {
-    auto kern = fa::fa_cache_many_kernel<D, BF16>;
-    int rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done);
-    if (rc) return rc;
-    kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
-  }
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (join) {
-    fa::fa_cache_join_kernel<D, BF16, L::kRows><<<fa::kCacheCtas, 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  }
-  return FA_OK;
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  };
+  int rc;
+  if constexpr (R == 256)
+    rc = run(fa::fa_cache_many_kernel<D, BF16>);
+  else
+    rc = run(fa::fa_cache_few_kernel<D, BF16, R>);
+  if (rc || !join) return rc;
+  fa::fa_cache_join_kernel<D, BF16, R><<<fa::kCacheCtas, 256, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 template <int D, bool BF16>
-int dispatch_cache(bool few, const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams& p, bool join, int dev,
+int dispatch_cache(int rows, const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams& p, bool join, int dev,
                    cudaStream_t s) {
-  return few ? launch_cache<D, BF16, true>(tk, tv, p, join, dev, s)
-             : launch_cache<D, BF16, false>(tk, tv, p, join, dev, s);
+  switch (rows) {
+    case 8: return launch_cache<D, BF16, 8>(tk, tv, p, join, dev, s);
+    case 16: return launch_cache<D, BF16, 16>(tk, tv, p, join, dev, s);
+    case 32: return launch_cache<D, BF16, 32>(tk, tv, p, join, dev, s);
+    default: return launch_cache<D, BF16, 256>(tk, tv, p, join, dev, s);
+  }
 }
 
 template <int D, bool BF16>
@@ -736,7 +738,7 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
 
 size_t fa_cache_workspace_size(int B, int Sq, int H, int Hkv, int D) {
   if (check_cache_queries(B, Sq, H, Hkv, D) != FA_OK) return 0;
-  return cache_layout(Sq * (H / Hkv) <= kFewRows ? kFewRows : kManyRows, D).total;
+  return cache_layout(cache_rows(Sq * (H / Hkv)), D).total;
 }
 
 int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
@@ -750,8 +752,7 @@ int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const 
     rc = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, num_pages, page, max_pages);
   if (rc) return rc;
   const int capacity = max_pages * page, n_rows = Sq * (H / Hkv);
-  const bool few = n_rows <= kFewRows;
-  const int rows = few ? kFewRows : kManyRows;
+  const int rows = cache_rows(n_rows);
   const int n_mt = (n_rows + rows - 1) / rows;
   if ((double)B * n_mt * Hkv * (capacity / 128 + 2) > 2147483647.0 * fa::kCacheCtas) return FA_ERR_INVALID;
   const CacheLayout lay = cache_layout(rows, D);
@@ -791,10 +792,10 @@ int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const 
   p.scale_log2 = scale * fa::kLog2e;
   const bool join = capacity > 128;  // units of one tile are never cut
   if (D == 64)
-    return dtype == FA_BF16 ? dispatch_cache<64, true>(few, tk, tv, p, join, dev, stream)
-                            : dispatch_cache<64, false>(few, tk, tv, p, join, dev, stream);
-  return dtype == FA_BF16 ? dispatch_cache<128, true>(few, tk, tv, p, join, dev, stream)
-                          : dispatch_cache<128, false>(few, tk, tv, p, join, dev, stream);
+    return dtype == FA_BF16 ? dispatch_cache<64, true>(rows, tk, tv, p, join, dev, stream)
+                            : dispatch_cache<64, false>(rows, tk, tv, p, join, dev, stream);
+  return dtype == FA_BF16 ? dispatch_cache<128, true>(rows, tk, tv, p, join, dev, stream)
+                          : dispatch_cache<128, false>(rows, tk, tv, p, join, dev, stream);
 }
 
 }  // extern "C"

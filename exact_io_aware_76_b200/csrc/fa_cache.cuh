@@ -365,11 +365,11 @@ __global__ void __launch_bounds__(256) fa_cache_join_kernel(const CacheParams p)
 // --------------------------------------------------------------------------------------------- shared pieces
 constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A in e5m2 (B in e4m3)
 
-// kFew: at most 32 query rows per unit (decoding); else blocks of 256 rows (chunks of prompts).
-template <int D, bool kBF16, bool kFew>
+// R: query rows per unit: 8, 16 or 32 (decoding), or blocks of 256 (chunks of prompts).
+template <int D, bool kBF16, int R>
 struct CacheSmem {
   static constexpr int kParts = kBF16 ? 2 : 3;       // e4m3 parts of q and of the probabilities
-  static constexpr int kRows = kFew ? 32 : 256;
+  static constexpr bool kFew = R <= 32;
   static constexpr int kNQ = kFew ? 1 : 2;           // 128-row Q tiles
   static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
   static constexpr int kStages = (kFew && kBF16) ? 5 : 4;
@@ -589,21 +589,22 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 }
 
 // -------------------------------------------------------------------------------- attention of few query rows
-// Decoding: up to 32 rows (the query heads of a K/V head, times a few tokens) against a long cache. The bytes of the cache
-// bound it, so everything else is arranged to hide behind the copies. An M = 128 product costs the same however few of
-// its rows are used, so the rows are put into the A operand four times, at lanes 0, 32, 64 and 96, and each warp
-// of the softmax warpgroup takes 32 of the tile's 128 keys for its copy: four warps share a tile's exponentials
-// without exchanging anything, each with its own running maximum, sum and rows of O (its P is 0 at the
-// other warps' keys). The four are joined once, at the end of the unit.
+// Decoding: up to R = 8, 16 or 32 rows (the query heads of a K/V head, times a few tokens) against a long cache. The
+// bytes of the cache bound it, so everything else is arranged to hide behind the copies. An M = 128 product costs the
+// same however few of its rows are used, so the rows are put into the A operand 128 / R times, and every copy takes
+// another R of the tile's 128 keys: lane = (copy, row), with a running maximum, sum and row of O of its own, and weights
+// of 0 for the other copies' keys. A lane computes R exponentials per tile, none twice and none idle, and the lanes exchange
+// nothing until the copies are joined, once, at the end of the unit.
 //
 // Warps: 0-3 softmax, 4 TMA, 5 MMA, 6 cleaner (see cache_cleaner), 7 idle.
-// TMEM columns: S in two buffers [0,128) and [128,256), O [256,384), parts of P from 384, 32 columns each.
-template <int D, bool kBF16>
+// TMEM columns: S in two buffers [0,128) and [128,256), O [256,384); the parts of P overwrite their S, 32 columns each.
+// With two buffers the softmax of tile g+1 runs while the tensor core does tile g's PV product and tile g+2's scores.
+template <int D, bool kBF16, int R>
 __global__ void __launch_bounds__(256, 1)
     fa_cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const CacheParams p) {
-  using L = CacheSmem<D, kBF16, true>;
-  constexpr int kStages = L::kStages, kParts = L::kParts, kRows = L::kRows;
+  using L = CacheSmem<D, kBF16, R>;
+  constexpr int kStages = L::kStages, kParts = L::kParts, kSlots = 32 / R, kCopies = 4 * kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -612,15 +613,16 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* kv_empty = v_full + kStages;
   uint64_t* v_clean = kv_empty + kStages;
   uint64_t* s_full = v_clean + kStages;   // [2]
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = s_full + 3;
-  uint64_t* q_ready = s_full + 4;
-  uint64_t* joint = s_full + 5;           // the four softmax warps among themselves
-  uint64_t* mma_done = s_full + 6;
+  uint64_t* p_full = s_full + 2;          // [2] (a warp may publish tile g + 1 before another has published tile g)
+  uint64_t* o_full = s_full + 4;
+  uint64_t* q_ready = s_full + 5;
+  uint64_t* joint = s_full + 6;           // the four softmax warps among themselves
+  uint64_t* unit_done = s_full + 7;       // a unit's products complete
+  uint64_t* mma_done = s_full + 8;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [32]
-  float* q_m = row_back + 32;                                     // [4][32]
-  float* q_l = q_m + 128;                                         // [4][32]
+  float* q_m = row_back + 32;                                     // [128 lanes]
+  float* q_l = q_m + 128;                                         // [128 lanes]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
 
@@ -634,10 +636,12 @@ __global__ void __launch_bounds__(256, 1)
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(p_full, 128);
+    mbar_init(&p_full[0], 128);
+    mbar_init(&p_full[1], 128);
     mbar_init(o_full, 1);
     mbar_init(q_ready, 128);
     mbar_init(joint, 128);
+    mbar_init(unit_done, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -650,16 +654,16 @@ __global__ void __launch_bounds__(256, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
-                                                     reinterpret_cast<CacheRun*>(smem + L::kRunOff));
+  const CacheRun run = cache_run<R, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
+                                                 reinterpret_cast<CacheRun*>(smem + L::kRunOff));
   if (run.count > 0) {
     if (warp == 4) {
       if (lane == 0) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      cache_producer<kRows, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
-                                     kv_empty, abort_flag);
+      cache_producer<R, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full, kv_empty,
+                                 abort_flag);
     } else if (warp == 5 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(256, 1)
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
-      const uint32_t o_tmem = tmem + 256, p_tmem = tmem + 384;
+      const uint32_t o_tmem = tmem + 256;
       auto issue_s = [&](int g) {
         const uint64_t b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
 #pragma unroll
@@ -675,11 +679,10 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             umma_ss_f8(tmem + (g & 1) * 128, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
-                       id_s | (q < 2 ? 0u : kE5M2A),
-                       (q > 0 || kk > 0) ? 1u : 0u);
+                       id_s | (q < 2 ? 0u : kE5M2A), (q > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&s_full[g & 1]);
       };
-      CacheWalk<kRows> walk;
+      CacheWalk<R> walk;
       walk.start(p, run.first);
       bool ok = true;
       for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
@@ -692,127 +695,140 @@ __global__ void __launch_bounds__(256, 1)
         for (int it = 0; it < left; ++it, ++g) {
           const int s = g % kStages;
           if (it + 1 < left) {
-            // The other S buffer was read before the previous tile's weights were published.
+            // Into the other buffer: the product that read the weights there was issued before.
             if (!mbar_wait(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
             issue_s(g + 1);
           }
           if (!mbar_wait(&v_clean[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
-          if (!mbar_wait(p_full, g & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
           const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
 #pragma unroll
           for (int q = 0; q < kParts; ++q)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts_f8(o_tmem, p_tmem + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
-                         id_o | (q < 2 ? 0u : kE5M2A),
-                         (it > 0 || q > 0 || kk > 0) ? 1u : 0u);
+              umma_ts_f8(o_tmem, tmem + (g & 1) * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
+                         id_o | (q < 2 ? 0u : kE5M2A), (it > 0 || q > 0 || kk > 0) ? 1u : 0u);
           umma_commit(o_full);
           umma_commit(&kv_empty[s]);
         }
+        umma_commit(unit_done);
         if (ok && g < run.count) walk.advance(p, left);
       }
       umma_commit(mma_done);
       int drain = 0;
       mbar_wait(mma_done, 0, &drain);
     } else if (warp == 6) {
-      cache_cleaner<kRows, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
+      cache_cleaner<R, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
     } else if (warp < 4) {
-      // ---------------------------------------------------------------- softmax
+      // ---------------------------------------------------------------- softmax (lane = copy, row)
       const uint32_t lane_base = tmem + ((warp * 32) << 16);
-      const uint32_t o_tmem = lane_base + 256, p_tmem = lane_base + 384;
-      {
-        // This warp's rows of P are 0 but at its own keys (columns 8 * warp .. + 7 of each part).
-        uint32_t z[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0u;
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) tmem_st_x32(p_tmem + q * 32, z);
-        tmem_st_wait();
-      }
+      const uint32_t o_tmem = lane_base + 256;
+      const int slot = lane / R, r = lane % R;
       int joins = 0;
       auto join = [&]() {  // all 128 threads of these warps, bounded like every wait
         mbar_arrive(joint);
         return mbar_wait(joint, joins++ & 1, abort_flag);
       };
-      CacheWalk<kRows> walk;
-      walk.start(p, run.first);
-      bool ok = true;
-      for (int g = 0; ok && g < run.count;) {
-        const CacheItem t = walk.item;
-        const int hk = walk.at.hk, w0 = walk.at.w;
-        const int left = min(run.count - g, t.n - w0);
-        // ---- q: four threads per row; each row goes to its four places in the A operand
-        {
-          const int r = threadIdx.x >> 2, piece = threadIdx.x & 3;
-          constexpr int kVec = D / 32;  // 16-byte pieces of 8 elements per thread
-          uint4 v[kVec];
-          uint32_t amax = 0;
+      // q of a unit into the A operand: 128 / R threads per row, each row to its 128 / R places. The previous unit's
+      // scores must be complete.
+      auto load_q = [&](const CacheItem& t, int hk) {
+        constexpr int kPer = D * R / 128;   // elements per thread: 8 .. 32, or 4 (R = 8, D = 64: half the threads idle)
+        constexpr int kVec = kPer >= 8 ? kPer / 8 : 1;
+        constexpr int kThreadsPerRow = D / (8 * kVec);
+        const int row_q = threadIdx.x / kThreadsPerRow, piece = threadIdx.x % kThreadsPerRow;
+        uint4 v[kVec];
+        uint32_t amax = 0;
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < t.rows) {
-            const int row = t.row0 + r, qi = row / p.group, h = hk * p.group + row % p.group;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(p.q) + ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D) + piece * kVec;
+        for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row_q < t.rows) {
+          const int row = t.row0 + row_q, qi = row / p.group, h = hk * p.group + row % p.group;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                            ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D) +
+                             piece * kVec;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] = src[i];
+          for (int i = 0; i < kVec; ++i) v[i] = src[i];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
-          }
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          float mul, back;
-          q_row_scale(amax, mul, back);
-          if (piece == 0) row_back[r] = back * p.scale_log2;
+          for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
+        }
+#pragma unroll
+        for (int s = 1; s < kThreadsPerRow; s <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+        float mul, back;
+        q_row_scale(amax, mul, back);
+        if (row_q < R) {
+          if (piece == 0) row_back[row_q] = back * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             uint2 part[kParts];
             q_split8<kBF16, kParts>(v[i], mul, part);
             const int e8 = piece * kVec + i;  // 8-byte unit of the row
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int m = c * 32 + r;
+            for (int c = 0; c < kCopies; ++c) {
+              const int m = c * R + row_q;
               uint8_t* dst = smem + L::kQOff + m * 128 + ((e8 >> 1) ^ (m & 7)) * 16 + (e8 & 1) * 8;
 #pragma unroll
               for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q];
             }
           }
-          fence_proxy_async_smem();
-          mbar_arrive(q_ready);
-          if (!join()) { ok = false; break; }
         }
-        const float c_row = row_back[lane];
-        const int row = t.row0 + min(static_cast<int>(lane), t.rows - 1);
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready);
+      };
+      CacheWalk<R> walk;
+      walk.start(p, run.first);
+      load_q(walk.item, walk.at.hk);
+      bool ok = join();
+      for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
+        const CacheItem t = walk.item;
+        const int hk = walk.at.hk, w0 = walk.at.w;
+        const int left = min(run.count - g, t.n - w0);
+        const float c_row = row_back[r];
+        const int row = t.row0 + min(r, t.rows - 1);
         const int aligned = t.c0 + row / p.group;
         const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
         float m = -INFINITY, l = 0.f;
         for (int it = 0; it < left; ++it, ++g) {
           const int s = g % kStages;
-          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * warp;
+          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * warp + R * slot;
           if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag) ||
               !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          float x[32];
-          tmem_ld_x32(lane_base + (g & 1) * 128 + 32 * warp, reinterpret_cast<uint32_t*>(x));
-          const float* f = fac + s * 24 + 2 * warp;
-          const float a0 = c_row * f[0], a1 = c_row * f[1], lv0 = f[8], lv1 = f[9], iv0 = f[16], iv1 = f[17];
+          float x[R];
+          {
+            float v[32];
+            tmem_ld_x32(lane_base + (g & 1) * 128 + 32 * warp, reinterpret_cast<uint32_t*>(v));
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+              if (R == 32) x[c] = v[c];
+              if (R == 16) x[c] = slot ? v[(c + 16) % 32] : v[c];
+              if (R == 8) {
+                const float lo = (slot & 1) ? v[(c + 8) % 32] : v[c], hi = (slot & 1) ? v[(c + 24) % 32] : v[(c + 16) % 32];
+                x[c] = (slot & 2) ? hi : lo;
+              }
+            }
+          }
+          // this lane's 16-key groups: one (R <= 16) or two
+          const float* f = fac + s * 24 + 2 * warp + (R * slot) / 16;
+          const float a0 = c_row * f[0], lv0 = f[8], iv0 = f[16];
+          const float a1 = R == 32 ? c_row * f[1] : a0, lv1 = R == 32 ? f[9] : lv0, iv1 = R == 32 ? f[17] : iv0;
           const bool masked = tile0 + 127 > t.c_min ||
                               (p.win_left >= 0 && tile0 < t.c_max - p.win_left && tile0 + 127 >= p.sinks);
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
+          for (int c = 0; c < R; ++c) {
             x[c] = fmaf(x[c], c < 16 ? a0 : a1, c < 16 ? lv0 : lv1);
             if (masked && (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks))) x[c] = -INFINITY;
             mx = fmaxf(mx, x[c]);
           }
           const float m_new = fmaxf(m, mx);
-          // The previous tile's product has to be done with P and O.
-          if (it > 0 && !mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after_sync();
           if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
             const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
             if (it > 0) {
+              // O has to hold the previous tile's product. (This tile's scores came after the product before that,
+              // so the barrier is at most one phase behind.)
+              if (!mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
+              tc_fence_after_sync();
 #pragma unroll
               for (int c0 = 0; c0 < D; c0 += 32) {
                 float o[32];
@@ -827,9 +843,9 @@ __global__ void __launch_bounds__(256, 1)
           }
           const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
           float sum0 = 0.f, sum1 = 0.f;
-          uint32_t pk[kParts][8];
+          uint32_t pk[kParts][8];  // this warp's 32 keys of the row: zeros but for the lane's own
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
+          for (int c = 0; c < R; c += 4) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[c + e] + off);
@@ -837,65 +853,81 @@ __global__ void __launch_bounds__(256, 1)
             uint32_t part[kParts];
             p_split4<kParts>(w[0], w[1], w[2], w[3], part);
 #pragma unroll
-            for (int q = 0; q < kParts; ++q) pk[q][c / 4] = part[q];
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+              for (int k = 0; k < kSlots; ++k) pk[q][k * (R / 4) + c / 4] = k == slot ? part[q] : 0u;
           }
           l += sum0 * iv0 + sum1 * iv1;
+          const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) tmem_st_x8(p_tmem + q * 32 + 8 * warp, pk[q]);
+          for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t at = lane_base + (g & 1) * 128 + q * 32 + 8 * k;
+              if (k == static_cast<int>(warp))
+                tmem_st_x8(at, pk[q]);
+              else
+                tmem_st_x8(at, zero);
+            }
           tmem_st_wait();
           tc_fence_before_sync();
-          mbar_arrive(p_full);
+          mbar_arrive(&p_full[g & 1]);
         }
         if (!ok) break;
-        // ---- the unit's (or piece's) end: join the four quarters
+        // ---- the unit's (or piece's) end. The next unit's q first: its scores can run during the join.
         q_m[warp * 32 + lane] = m;
         q_l[warp * 32 + lane] = l;
+        const bool whole = left == t.n, more = g < run.count;
+        if (more) {
+          walk.advance(p, left);
+          load_q(walk.item, walk.at.hk);
+        }
         if (!join()) { ok = false; break; }
         float m_all = -INFINITY, l_all = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m_all = fmaxf(m_all, q_m[q * 32 + lane]);
+        for (int q = 0; q < kCopies; ++q) m_all = fmaxf(m_all, q_m[q * R + r]);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) l_all += q_l[q * 32 + lane] * ex2_approx(q_m[q * 32 + lane] - m_use);
-        const bool whole = left == t.n;
+        for (int q = 0; q < kCopies; ++q) l_all += q_l[q * R + r] * ex2_approx(q_m[q * R + r] - m_use);
         float f = ex2_approx(m - m_use);
         if (whole) f *= l_all == 0.f ? 0.f : 1.f / l_all;  // l = 0: no visible key (a NaN stays one)
-        const size_t slot = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * kRows;
+        const size_t slot0 = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * R;
         if (warp == 0 && static_cast<int>(lane) < t.rows) {
           if (whole) {
             const int h = hk * p.group + row % p.group, qi = row / p.group;
             p.lse[(static_cast<size_t>(t.b) * p.H + h) * p.Sq + qi] =
                 l_all == 0.f ? -INFINITY : (m_all + log2f(l_all) - kCacheShift) * kLn2;
           } else {
-            *reinterpret_cast<float2*>(p.part_ml + (slot + lane) * 2) = make_float2(m_all, l_all);
+            *reinterpret_cast<float2*>(p.part_ml + (slot0 + lane) * 2) = make_float2(m_all, l_all);
           }
         }
-        if (!mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
+        // (not o_full: the last product but one may be open too, and its phase would be taken for the last one's)
+        if (!mbar_wait(unit_done, unit & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
         float* xo = reinterpret_cast<float*>(smem + L::kXOff);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
           tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-          // (a quarter that saw no key of this row has f = 0, and weights 0: its O is 0)
+          // (a copy that saw no key of this row has f = 0, and weights 0: its O is 0)
 #pragma unroll
           for (int c = 0; c < 32; ++c) xo[(warp * 32 + lane) * 33 + c] = o[c] * f;
           if (!join()) { ok = false; break; }
-          for (int r = warp; r < t.rows; r += 4) {
-            const float v = (xo[r * 33 + lane] + xo[(32 + r) * 33 + lane]) +
-                            (xo[(64 + r) * 33 + lane] + xo[(96 + r) * 33 + lane]);
+          for (int ro = warp; ro < t.rows; ro += 4) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < kCopies; ++q) v += xo[(q * R + ro) * 33 + lane];
             if (whole) {
-              const int rr = t.row0 + r, qi = rr / p.group, h = hk * p.group + rr % p.group;
+              const int rr = t.row0 + ro, qi = rr / p.group, h = hk * p.group + rr % p.group;
               static_cast<uint16_t*>(p.out)[((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + c0 + lane] =
                   static_cast<uint16_t>(pack2<kBF16>(v, 0.f));
             } else {
-              p.part_o[(slot + r) * D + c0 + lane] = v;
+              p.part_o[(slot0 + ro) * D + c0 + lane] = v;
             }
           }
           if (!join()) { ok = false; break; }
         }
-        if (!ok) break;
-        if (g < run.count) walk.advance(p, left);
+        tc_fence_before_sync();
       }
     }
   }
@@ -918,8 +950,9 @@ template <int D, bool kBF16>
 __global__ void __launch_bounds__(384, 1)
     fa_cache_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const CacheParams p) {
-  using L = CacheSmem<D, kBF16, false>;
-  constexpr int kStages = L::kStages, kParts = L::kParts, kRows = L::kRows;
+  constexpr int kRows = 256;
+  using L = CacheSmem<D, kBF16, kRows>;
+  constexpr int kStages = L::kStages, kParts = L::kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
