@@ -7,7 +7,7 @@
 // Attention without converting the cache. K and V stay e4m3 all the way into the tensor core (tcgen05 kind::f8f6f4);
 // it is the other operand that is brought to 8 bits, without loss: a 16-bit number has 8 (bf16) or 11 (fp16)
 // significant bits and an e4m3 number 4, so q = q1 + q2 (+ q3) with q1 = e4m3(q), q2 = e4m3(q - q1) and, for fp16,
-// q3 = e5m2(q - q1 - q2) (3 bits are left, and e5m2 reaches further down) is exact as long as the parts stay in range.
+// a third part for the 3 bits left is exact as long as the parts stay in range (split_f16x2).
 // Each query row is first scaled by a power of two that brings its largest element to [128, 256); elements below
 // 2^-9 of the largest lose what falls under the last part's smallest step, an absolute error of at most 2^-17 (bf16) or
 // 2^-24 (fp16) of the row's largest element. S = q K^T is the sum of the parts' products in the fp32 accumulator.
@@ -85,6 +85,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Parts beyond the stacked ones: the third part of fp16 where it has no rows of its own.
+__host__ __device__ constexpr bool part_is_e5m2(int q, int stack) { return q == 2 && stack < 3; }
 template <bool kBF16>
 __device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
   if (kBF16) {
@@ -371,23 +378,26 @@ struct CacheSmem {
   static constexpr int kParts = kBF16 ? 2 : 3;       // e4m3 parts of q and of the probabilities
   static constexpr bool kFew = R <= 32;
   static constexpr int kNQ = kFew ? 1 : 2;           // 128-row Q tiles
+  // Few rows: the A operand holds every row 128 / R times, kStack of them with different parts.
+  static constexpr int kStack = R == 8 ? (kParts == 3 ? 4 : 2) : R == 16 ? 2 : 1;
+  static constexpr int kPass = (kParts + kStack - 1) / kStack;  // products per S or O
   static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
-  static constexpr int kStages = (kFew && kBF16) ? 5 : 4;
-  static constexpr int kQOff = 0;                    // [part][Q tile]
-  static constexpr int kKOff = kQOff + kParts * kNQ * kTile;
+  static constexpr int kStages = kFew && kPass == 1 ? 5 : 4;
+  static constexpr int kQOff = 0;                    // [product][Q tile]
+  static constexpr int kKOff = kQOff + kPass * kNQ * kTile;
   static constexpr int kVOff = kKOff + kStages * kTile;
-  static constexpr int kXOff = kVOff + kStages * kTile;  // kFew: the quarters' sums, 4 x 32 rows x 33 floats
-  static constexpr int kXBytes = kFew ? 4 * 32 * 33 * 4 : 0;
+  static constexpr int kXOff = kVOff + kStages * kTile;  // kFew: 32 columns of all copies' O, 256 lanes x 33 floats
+  static constexpr int kXBytes = kFew ? 256 * 33 * 4 : 0;
   static constexpr int kFacOff = kXOff + kXBytes;    // per stage: k factor, log2 v scale, 1 / v scale of 8 key groups
-  static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per quarter [2][4][32]
-  static constexpr int kMlBytes = kFew ? (32 + 256) * 4 : 0;
+  static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per lane [2][256]
+  static constexpr int kMlBytes = kFew ? (32 + 512) * 4 : 0;
   static constexpr int kBarOff = kMlOff + kMlBytes;
   static constexpr int kNumBars = 4 * kStages + 11;
   static constexpr int kRunOff = kBarOff + kNumBars * 8;
   static constexpr int kScanOff = kRunOff + 16;
   static constexpr int kMiscOff = kScanOff + 13 * 8;
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
-  static constexpr int kThreads = kFew ? 256 : 384;
+  static constexpr int kThreads = 384;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -538,27 +548,41 @@ __device__ __forceinline__ void q_row_scale(uint32_t amax_bits, float& mul, floa
   }
 }
 
-// Eight elements of q (16 bytes) -> kParts x 8 e4m3 codes.
-template <bool kBF16, int kParts>
+// Two fp16 numbers -> kParts pairs of 8-bit codes, largest part first. Part q is multiplied by 2^(4 (q % kStack)), so
+// that the parts that lie in different rows of an operand (kStack of them) all use the whole e4m3 range; a part behind
+// them adds to the first one's row, unscaled, in e5m2.
+template <int kParts, int kStack>
+__device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t* code) {
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    constexpr uint32_t kUp[4] = {0x3c003c00u, 0x4c004c00u, 0x5c005c00u, 0x6c006c00u};    // 1, 2^4, 2^8, 2^12
+    constexpr uint32_t kDown[4] = {0x3c003c00u, 0x2c002c00u, 0x1c001c00u, 0x0c000c00u};  // 1, 2^-4, 2^-8, 2^-12
+    const uint32_t up = q % kStack ? mul_f16x2(h, kUp[q % kStack]) : h;
+    if (part_is_e5m2(q, kStack)) {
+      code[q] = e5m2x2_from_f16x2(up);
+    } else {
+      code[q] = e4m3x2_from_f16x2(up);
+      if (q + 1 < kParts) {
+        const uint32_t back = f16x2_from_e4m3x2(code[q]);
+        h = sub_f16x2(h, q % kStack ? mul_f16x2(back, kDown[q % kStack]) : back);
+      }
+    }
+  }
+}
+
+// Eight elements of q (16 bytes) -> kParts x 8 codes.
+template <bool kBF16, int kParts, int kStack>
 __device__ __forceinline__ void q_split8(const uint4& v, float mul, uint2* part) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t h[4];
+  uint32_t c[4][kParts];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float a, b;
     unpack2<kBF16>(w[i], a, b);
-    h[i] = pack2_f16(a * mul, b * mul);  // at most 256, 11 significant bits: exact down to 2^-24
+    split_f16x2<kParts, kStack>(pack2_f16(a * mul, b * mul), c[i]);  // at most 256, 11 bits: exact down to 2^-24
   }
 #pragma unroll
-  for (int q = 0; q < kParts; ++q) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = q < 2 ? e4m3x2_from_f16x2(h[i]) : e5m2x2_from_f16x2(h[i]);
-      if (q + 1 < kParts) h[i] = sub_f16x2(h[i], f16x2_from_e4m3x2(c[i]));
-    }
-    part[q] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  }
+  for (int q = 0; q < kParts; ++q) part[q] = make_uint2(c[0][q] | (c[1][q] << 16), c[2][q] | (c[3][q] << 16));
 }
 template <bool kBF16>
 __device__ __forceinline__ uint32_t q_amax8(const uint4& v, uint32_t amax) {
@@ -572,39 +596,41 @@ __device__ __forceinline__ uint32_t q_amax8(const uint4& v, uint32_t amax) {
   return amax;
 }
 
-// Four weights -> their e4m3 parts, packed four to a register (first weight lowest).
-template <int kParts>
+// Four weights -> their parts' codes, packed four to a register (first weight lowest).
+template <int kParts, int kStack>
 __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uint32_t* part) {
-  uint32_t h0 = pack2_f16(a, b), h1 = pack2_f16(c, d);
+  uint32_t lo[kParts], hi[kParts];
+  split_f16x2<kParts, kStack>(pack2_f16(a, b), lo);
+  split_f16x2<kParts, kStack>(pack2_f16(c, d), hi);
 #pragma unroll
-  for (int q = 0; q < kParts; ++q) {
-    const uint32_t c0 = q < 2 ? e4m3x2_from_f16x2(h0) : e5m2x2_from_f16x2(h0);
-    const uint32_t c1 = q < 2 ? e4m3x2_from_f16x2(h1) : e5m2x2_from_f16x2(h1);
-    part[q] = c0 | (c1 << 16);
-    if (q + 1 < kParts) {
-      h0 = sub_f16x2(h0, f16x2_from_e4m3x2(c0));
-      h1 = sub_f16x2(h1, f16x2_from_e4m3x2(c1));
-    }
-  }
+  for (int q = 0; q < kParts; ++q) part[q] = lo[q] | (hi[q] << 16);
 }
 
 // -------------------------------------------------------------------------------- attention of few query rows
 // Decoding: up to R = 8, 16 or 32 rows (the query heads of a K/V head, times a few tokens) against a long cache. The
 // bytes of the cache bound it, so everything else is arranged to hide behind the copies. An M = 128 product costs the
-// same however few of its rows are used, so the rows are put into the A operand 128 / R times, and every copy takes
-// another R of the tile's 128 keys: lane = (copy, row), with a running maximum, sum and row of O of its own, and weights
-// of 0 for the other copies' keys. A lane computes R exponentials per tile, none twice and none idle, and the lanes exchange
-// nothing until the copies are joined, once, at the end of the unit.
+// same however few of its rows are used, so the rows are put into the A operand 128 / R times. kStack neighbouring
+// copies hold the parts of q (and later of the weights), so that one product does the work of all parts: their partial
+// scores are added across lanes, and their rows of O at the end. The other copies share out the tile's 128 keys: each
+// warp has 32, and where copies are left its lanes take 16 each; a copy has a running maximum, sum and rows of O of its
+// own, and weights of 0 for the others' keys. Nothing else is exchanged until the copies are joined, once, at the end of
+// the unit. (One product with all parts instead of one per part: 32 x 32768 tokens, 64 query heads on 8, bf16:
+// 505 -> TODO us; an M = N = 128, K = 32 product of 8-bit operands takes 115 to 140 cycles here, so the products were the bound.)
 //
-// Warps: 0-3 softmax, 4 TMA, 5 MMA, 6 cleaner (see cache_cleaner), 7 idle.
-// TMEM columns: S in two buffers [0,128) and [128,256), O [256,384); the parts of P overwrite their S, 32 columns each.
-// With two buffers the softmax of tile g+1 runs while the tensor core does tile g's PV product and tile g+2's scores.
+// Warps: 0-3 and 4-7 softmax of the even and the odd tiles of the run, each warpgroup with its own S and O (so its own
+// maxima and sums too, joined with the others at the end): two tiles are in work at any time, and a warpgroup's
+// latencies have two tiles' time to pass in. 8 TMA, 9 MMA, 10 cleaner (see cache_cleaner), 11 idle.
+// TMEM columns: S of both [0,128) and [128,256), O [256,384) and [384,512); the parts of P overwrite their S, 32 columns
+// each. The MMA order is S(g+1), PV(g), S(g+2), ..., so when S(g) has arrived PV(g-2), the last product of that
+// warpgroup, is complete: O may be rescaled without a further wait.
 template <int D, bool kBF16, int R>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(384, 1)
     fa_cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const CacheParams p) {
   using L = CacheSmem<D, kBF16, R>;
-  constexpr int kStages = L::kStages, kParts = L::kParts, kSlots = 32 / R, kCopies = 4 * kSlots;
+  constexpr int kStages = L::kStages, kParts = L::kParts, kStack = L::kStack, kPass = L::kPass;
+  constexpr int kSlots = 32 / R, kCopies = 8 * kSlots;  // copies per warp, in all (both warpgroups)
+  constexpr int kKeys = 32 * kStack / kSlots;           // keys per lane and tile: 16 or 32
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -613,16 +639,15 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* kv_empty = v_full + kStages;
   uint64_t* v_clean = kv_empty + kStages;
   uint64_t* s_full = v_clean + kStages;   // [2]
-  uint64_t* p_full = s_full + 2;          // [2] (a warp may publish tile g + 1 before another has published tile g)
-  uint64_t* o_full = s_full + 4;
-  uint64_t* q_ready = s_full + 5;
-  uint64_t* joint = s_full + 6;           // the four softmax warps among themselves
-  uint64_t* unit_done = s_full + 7;       // a unit's products complete
-  uint64_t* mma_done = s_full + 8;
+  uint64_t* p_full = s_full + 2;          // [2]
+  uint64_t* q_ready = s_full + 4;
+  uint64_t* joint = s_full + 5;           // the softmax warps among themselves
+  uint64_t* unit_done = s_full + 6;       // a unit's products complete
+  uint64_t* mma_done = s_full + 7;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [32]
-  float* q_m = row_back + 32;                                     // [128 lanes]
-  float* q_l = q_m + 128;                                         // [128 lanes]
+  float* q_m = row_back + 32;                                     // [256 lanes]
+  float* q_l = q_m + 256;                                         // [256 lanes]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
 
@@ -638,15 +663,14 @@ __global__ void __launch_bounds__(256, 1)
     mbar_init(&s_full[1], 1);
     mbar_init(&p_full[0], 128);
     mbar_init(&p_full[1], 128);
-    mbar_init(o_full, 1);
-    mbar_init(q_ready, 128);
-    mbar_init(joint, 128);
+    mbar_init(q_ready, 256);
+    mbar_init(joint, 256);
     mbar_init(unit_done, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tmem_holder, L::kTmemCols);
     tmem_relinquish();
   }
@@ -656,30 +680,31 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t tmem = *tmem_holder;
   const CacheRun run = cache_run<R, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
                                                  reinterpret_cast<CacheRun*>(smem + L::kRunOff));
-  if (run.count > 0) {
-    if (warp == 4) {
+  if (warp >= 8) {
+    regs_dec<88>();
+    if (run.count == 0) {
+    } else if (warp == 8) {
       if (lane == 0) {
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
       cache_producer<R, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full, kv_empty,
                                  abort_flag);
-    } else if (warp == 5 && lane == 0) {
+    } else if (warp == 9 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
       constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
-      const uint32_t o_tmem = tmem + 256;
       auto issue_s = [&](int g) {
         const uint64_t b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+        for (int q = 0; q < kPass; ++q)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             umma_ss_f8(tmem + (g & 1) * 128, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
-                       id_s | (q < 2 ? 0u : kE5M2A), (q > 0 || kk > 0) ? 1u : 0u);
+                       id_s | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&s_full[g & 1]);
       };
       CacheWalk<R> walk;
@@ -705,12 +730,11 @@ __global__ void __launch_bounds__(256, 1)
           tc_fence_after_sync();
           const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
+          for (int q = 0; q < kPass; ++q)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts_f8(o_tmem, tmem + (g & 1) * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
-                         id_o | (q < 2 ? 0u : kE5M2A), (it > 0 || q > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(o_full);
+              umma_ts_f8(tmem + 256 + (g & 1) * 128, tmem + (g & 1) * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
+                         id_o | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (it > 1 || q > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&kv_empty[s]);
         }
         umma_commit(unit_done);
@@ -719,23 +743,26 @@ __global__ void __launch_bounds__(256, 1)
       umma_commit(mma_done);
       int drain = 0;
       mbar_wait(mma_done, 0, &drain);
-    } else if (warp == 6) {
+    } else if (warp == 10) {
       cache_cleaner<R, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
-    } else if (warp < 4) {
+    }
+  } else {
+    regs_inc<208>();
+    if (run.count > 0) {
       // ---------------------------------------------------------------- softmax (lane = copy, row)
-      const uint32_t lane_base = tmem + ((warp * 32) << 16);
-      const uint32_t o_tmem = lane_base + 256;
-      const int slot = lane / R, r = lane % R;
+      const int wg = warp / 4, quarter = warp % 4;  // even or odd tiles; keys 32 * quarter .. + 31 of a tile
+      const uint32_t lane_base = tmem + ((quarter * 32) << 16);
+      const uint32_t s_tmem = lane_base + wg * 128, o_tmem = lane_base + 256 + wg * 128;
+      const int r = lane % R, stack = lane / R % kStack, share = lane / (R * kStack);  // row, part, share of the keys
+      const float down = pow2i(-4 * stack);
       int joins = 0;
-      auto join = [&]() {  // all 128 threads of these warps, bounded like every wait
+      auto join = [&]() {  // all threads of these warps, bounded like every wait
         mbar_arrive(joint);
         return mbar_wait(joint, joins++ & 1, abort_flag);
       };
-      // q of a unit into the A operand: 128 / R threads per row, each row to its 128 / R places. The previous unit's
-      // scores must be complete.
+      // q of a unit into the A operand, each row to its 128 / R places. The previous unit's scores must be complete.
       auto load_q = [&](const CacheItem& t, int hk) {
-        constexpr int kPer = D * R / 128;   // elements per thread: 8 .. 32, or 4 (R = 8, D = 64: half the threads idle)
-        constexpr int kVec = kPer >= 8 ? kPer / 8 : 1;
+        constexpr int kVec = D * R > 256 * 8 ? D * R / (256 * 8) : 1;  // 8-element vectors per thread
         constexpr int kThreadsPerRow = D / (8 * kVec);
         const int row_q = threadIdx.x / kThreadsPerRow, piece = threadIdx.x % kThreadsPerRow;
         uint4 v[kVec];
@@ -760,15 +787,18 @@ __global__ void __launch_bounds__(256, 1)
           if (piece == 0) row_back[row_q] = back * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
-            uint2 part[kParts];
-            q_split8<kBF16, kParts>(v[i], mul, part);
+            uint2 part[kPass * kStack];
+            q_split8<kBF16, kParts, kStack>(v[i], mul, part);
+#pragma unroll
+            for (int q = kParts; q < kPass * kStack; ++q) part[q] = make_uint2(0u, 0u);
             const int e8 = piece * kVec + i;  // 8-byte unit of the row
 #pragma unroll
-            for (int c = 0; c < kCopies; ++c) {
+            for (int c = 0; c < 128 / R; ++c) {
               const int m = c * R + row_q;
               uint8_t* dst = smem + L::kQOff + m * 128 + ((e8 >> 1) ^ (m & 7)) * 16 + (e8 & 1) * 8;
 #pragma unroll
-              for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q];
+              for (int q = 0; q < kPass; ++q)
+                *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q * kStack + c % kStack];
             }
           }
         }
@@ -788,35 +818,35 @@ __global__ void __launch_bounds__(256, 1)
         const int aligned = t.c0 + row / p.group;
         const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
         float m = -INFINITY, l = 0.f;
-        for (int it = 0; it < left; ++it, ++g) {
-          const int s = g % kStages;
-          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * warp + R * slot;
-          if (!mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag) ||
-              !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+        const int first = (wg - g) & 1;  // this warpgroup's first tile of the unit
+        for (int it = first; it < left; it += 2) {
+          const int gi = g + it, s = gi % kStages;
+          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * quarter + kKeys * share;
+          if (!mbar_wait(&s_full[wg], (gi >> 1) & 1, abort_flag) ||
+              !mbar_wait(&k_full[s], (gi / kStages) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          float x[R];
+          float x[kKeys];
           {
             float v[32];
-            tmem_ld_x32(lane_base + (g & 1) * 128 + 32 * warp, reinterpret_cast<uint32_t*>(v));
+            tmem_ld_x32(s_tmem + 32 * quarter, reinterpret_cast<uint32_t*>(v));
 #pragma unroll
-            for (int c = 0; c < R; ++c) {
-              if (R == 32) x[c] = v[c];
-              if (R == 16) x[c] = slot ? v[(c + 16) % 32] : v[c];
-              if (R == 8) {
-                const float lo = (slot & 1) ? v[(c + 8) % 32] : v[c], hi = (slot & 1) ? v[(c + 24) % 32] : v[(c + 16) % 32];
-                x[c] = (slot & 2) ? hi : lo;
-              }
+            for (int c = 0; c < kKeys; ++c) {
+              x[c] = (kKeys == 16 && share) ? v[(c + 16) % 32] : v[c];
+              if (kStack > 1) x[c] *= down;
+#pragma unroll
+              for (int o = R; o < R * kStack; o *= 2) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
             }
           }
-          // this lane's 16-key groups: one (R <= 16) or two
-          const float* f = fac + s * 24 + 2 * warp + (R * slot) / 16;
+          // this lane's 16-key groups: one or two
+          const float* f = fac + s * 24 + 2 * quarter + share;
           const float a0 = c_row * f[0], lv0 = f[8], iv0 = f[16];
-          const float a1 = R == 32 ? c_row * f[1] : a0, lv1 = R == 32 ? f[9] : lv0, iv1 = R == 32 ? f[17] : iv0;
+          const float a1 = kKeys == 32 ? c_row * f[1] : a0, lv1 = kKeys == 32 ? f[9] : lv0;
+          const float iv1 = kKeys == 32 ? f[17] : iv0;
           const bool masked = tile0 + 127 > t.c_min ||
                               (p.win_left >= 0 && tile0 < t.c_max - p.win_left && tile0 + 127 >= p.sinks);
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < R; ++c) {
+          for (int c = 0; c < kKeys; ++c) {
             x[c] = fmaf(x[c], c < 16 ? a0 : a1, c < 16 ? lv0 : lv1);
             if (masked && (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks))) x[c] = -INFINITY;
             mx = fmaxf(mx, x[c]);
@@ -824,11 +854,7 @@ __global__ void __launch_bounds__(256, 1)
           const float m_new = fmaxf(m, mx);
           if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
             const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-            if (it > 0) {
-              // O has to hold the previous tile's product. (This tile's scores came after the product before that,
-              // so the barrier is at most one phase behind.)
-              if (!mbar_wait(o_full, (g - 1) & 1, abort_flag)) { ok = false; break; }
-              tc_fence_after_sync();
+            if (it >= 2) {
 #pragma unroll
               for (int c0 = 0; c0 < D; c0 += 32) {
                 float o[32];
@@ -843,42 +869,51 @@ __global__ void __launch_bounds__(256, 1)
           }
           const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
           float sum0 = 0.f, sum1 = 0.f;
-          uint32_t pk[kParts][8];  // this warp's 32 keys of the row: zeros but for the lane's own
+          uint32_t pk[kPass][8];  // this warp's 32 keys of the row: this lane's part, zeros but for its own keys
 #pragma unroll
-          for (int c = 0; c < R; c += 4) {
+          for (int c = 0; c < kKeys; c += 4) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[c + e] + off);
             (c < 16 ? sum0 : sum1) += (w[0] + w[1]) + (w[2] + w[3]);
-            uint32_t part[kParts];
-            p_split4<kParts>(w[0], w[1], w[2], w[3], part);
+            uint32_t part[kPass * kStack];
+            p_split4<kParts, kStack>(w[0], w[1], w[2], w[3], part);
 #pragma unroll
-            for (int q = 0; q < kParts; ++q)
+            for (int q = kParts; q < kPass * kStack; ++q) part[q] = 0u;
 #pragma unroll
-              for (int k = 0; k < kSlots; ++k) pk[q][k * (R / 4) + c / 4] = k == slot ? part[q] : 0u;
+            for (int q = 0; q < kPass; ++q) {
+              uint32_t mine = part[q * kStack];
+#pragma unroll
+              for (int k = 1; k < kStack; ++k) mine = k == stack ? part[q * kStack + k] : mine;
+#pragma unroll
+              for (int k = 0; k < 32 / kKeys; ++k) pk[q][k * (kKeys / 4) + c / 4] = k == share ? mine : 0u;
+            }
           }
           l += sum0 * iv0 + sum1 * iv1;
           const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
+          for (int q = 0; q < kPass; ++q)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t at = lane_base + (g & 1) * 128 + q * 32 + 8 * k;
-              if (k == static_cast<int>(warp))
+              const uint32_t at = s_tmem + q * 32 + 8 * k;
+              if (k == quarter)
                 tmem_st_x8(at, pk[q]);
               else
                 tmem_st_x8(at, zero);
             }
           tmem_st_wait();
           tc_fence_before_sync();
-          mbar_arrive(&p_full[g & 1]);
+          mbar_arrive(&p_full[wg]);
         }
         if (!ok) break;
+        g += left;
         // ---- the unit's (or piece's) end. The next unit's q first: its scores can run during the join.
         q_m[warp * 32 + lane] = m;
         q_l[warp * 32 + lane] = l;
         const bool whole = left == t.n, more = g < run.count;
         if (more) {
+          // (the last tile's scores may be the other warpgroup's)
+          if (!mbar_wait(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
           walk.advance(p, left);
           load_q(walk.item, walk.at.hk);
         }
@@ -888,8 +923,9 @@ __global__ void __launch_bounds__(256, 1)
         for (int q = 0; q < kCopies; ++q) m_all = fmaxf(m_all, q_m[q * R + r]);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
 #pragma unroll
-        for (int q = 0; q < kCopies; ++q) l_all += q_l[q * R + r] * ex2_approx(q_m[q * R + r] - m_use);
-        float f = ex2_approx(m - m_use);
+        for (int q = 0; q < kCopies; ++q)
+          if (q % kStack == 0) l_all += q_l[q * R + r] * ex2_approx(q_m[q * R + r] - m_use);
+        float f = ex2_approx(m - m_use) * down;
         if (whole) f *= l_all == 0.f ? 0.f : 1.f / l_all;  // l = 0: no visible key (a NaN stays one)
         const size_t slot0 = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * R;
         if (warp == 0 && static_cast<int>(lane) < t.rows) {
@@ -901,7 +937,6 @@ __global__ void __launch_bounds__(256, 1)
             *reinterpret_cast<float2*>(p.part_ml + (slot0 + lane) * 2) = make_float2(m_all, l_all);
           }
         }
-        // (not o_full: the last product but one may be open too, and its phase would be taken for the last one's)
         if (!mbar_wait(unit_done, unit & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
         float* xo = reinterpret_cast<float*>(smem + L::kXOff);
@@ -909,11 +944,12 @@ __global__ void __launch_bounds__(256, 1)
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
           tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-          // (a copy that saw no key of this row has f = 0, and weights 0: its O is 0)
+          // (A copy that saw no key of this row has f = 0, and weights 0: its O is 0. A warpgroup without a tile in
+          // this unit has no O at all.)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) xo[(warp * 32 + lane) * 33 + c] = o[c] * f;
+          for (int c = 0; c < 32; ++c) xo[(warp * 32 + lane) * 33 + c] = first < left ? o[c] * f : 0.f;
           if (!join()) { ok = false; break; }
-          for (int ro = warp; ro < t.rows; ro += 4) {
+          for (int ro = warp; ro < t.rows; ro += 8) {
             float v = 0.f;
 #pragma unroll
             for (int q = 0; q < kCopies; ++q) v += xo[(q * R + ro) * 33 + lane];
@@ -933,7 +969,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -1122,7 +1158,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           uint2 part[kParts];
-          q_split8<kBF16, kParts>(src[i], mul, part);
+          q_split8<kBF16, kParts, 1>(src[i], mul, part);
           uint8_t* dst = smem + L::kQOff + t * L::kTile + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kTile) = part[q];
@@ -1202,7 +1238,7 @@ __global__ void __launch_bounds__(384, 1)
               w3_ = ex2_approx(w3_);
               sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
               uint32_t part[kParts];
-              p_split4<kParts>(w0_, w1_, w2_, w3_, part);
+              p_split4<kParts, 1>(w0_, w1_, w2_, w3_, part);
 #pragma unroll
               for (int q = 0; q < kParts; ++q) pk[q][(c - 64 * half) / 4] = part[q];
             }
