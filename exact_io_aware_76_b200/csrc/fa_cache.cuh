@@ -15,11 +15,12 @@
 // 2^-11, set by their fp16 rounding before the split).
 //
 // Scales. With ks, vs the scales of key j's page and c = scale * log2 e, the weight that reaches the PV product is
-//   w_ij = 2^(s_ij c ks + log2 vs - m_i + 5),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
+//   w_ij = 2^(s_ij c ks + log2 vs - m_i + 6),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
 // with m_i the running maximum of s c ks + log2 vs: the V scale is part of the exponent, so pages of any scales share one
-// accumulator, and the largest weights have full precision whatever the scales are. The factor 2^5 uses
-// e4m3's range upwards (m may lag by up to 3, so w <= 2^8) and leaves 2^-14 .. 2^-9 below for small weights.
-// Scales lie in [2^-50, 2^50], so l (at most 2^(5+3+100) times the number of keys) stays finite.
+// accumulator, and the largest weights have full precision whatever the scales are. The factor 2^6 uses e4m3's
+// range upwards (m may lag by up to 2, so w <= 2^8); what small weights lose lies below 2^-20 of the largest (the
+// smallest half step of the last part, see split_f16x2), about 14 in the exponent of e.
+// Scales lie in [2^-50, 2^50], so l (at most 2^(6+2+100) times the number of keys) stays finite.
 //
 // Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
 // tiles, and before them the tiles with sinks). All units' tiles are laid end to end and every CTA takes an equal
@@ -32,8 +33,8 @@
 namespace fa {
 
 constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that the workspace size needs no device
-constexpr float kCacheLag = 3.0f;    // how far the running maximum may lag (log2)
-constexpr float kCacheShift = 5.0f;  // weights carry 2^5 (see above)
+constexpr float kCacheLag = 2.0f;    // how far the running maximum may lag (log2)
+constexpr float kCacheShift = 6.0f;  // weights carry 2^6 (see above)
 
 struct CacheParams {
   const void* q;         // [B, Sq, H, D]
@@ -375,16 +376,18 @@ constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A
 // R: query rows per unit: 8, 16 or 32 (decoding), or blocks of 256 (chunks of prompts).
 template <int D, bool kBF16, int R>
 struct CacheSmem {
-  static constexpr int kParts = kBF16 ? 2 : 3;       // e4m3 parts of q and of the probabilities
   static constexpr bool kFew = R <= 32;
   static constexpr int kNQ = kFew ? 1 : 2;           // 128-row Q tiles
-  // Few rows: the A operand holds every row 128 / R times, kStack of them with different parts.
-  static constexpr int kStack = R == 8 ? (kParts == 3 ? 4 : 2) : R == 16 ? 2 : 1;
-  static constexpr int kPass = (kParts + kStack - 1) / kStack;  // products per S or O
+  // Parts of q and of the weights. Few rows: the A operand holds every row 128 / R times, kStack of them with different
+  // parts. Where the parts are not stacked (and so not scaled) the weights get a third one for the sake of small weights.
+  static constexpr int kStack = R == 8 ? (kBF16 ? 2 : 4) : R == 16 ? 2 : 1;
+  static constexpr int kQParts = kBF16 ? 2 : 3, kPParts = kBF16 && kStack > 1 ? 2 : 3;
+  static constexpr int kQPass = (kQParts + kStack - 1) / kStack;  // products per S
+  static constexpr int kPPass = (kPParts + kStack - 1) / kStack;  // products per O
   static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
-  static constexpr int kStages = kFew && kPass == 1 ? 5 : 4;
+  static constexpr int kStages = kFew && kQPass == 1 ? 5 : 4;
   static constexpr int kQOff = 0;                    // [product][Q tile]
-  static constexpr int kKOff = kQOff + kPass * kNQ * kTile;
+  static constexpr int kKOff = kQOff + kQPass * kNQ * kTile;
   static constexpr int kVOff = kKOff + kStages * kTile;
   static constexpr int kXOff = kVOff + kStages * kTile;  // kFew: 32 columns of all copies' O, 256 lanes x 33 floats
   static constexpr int kXBytes = kFew ? 256 * 33 * 4 : 0;
@@ -550,7 +553,7 @@ __device__ __forceinline__ void q_row_scale(uint32_t amax_bits, float& mul, floa
 
 // Two fp16 numbers -> kParts pairs of 8-bit codes, largest part first. Part q is multiplied by 2^(4 (q % kStack)), so
 // that the parts that lie in different rows of an operand (kStack of them) all use the whole e4m3 range; a part behind
-// them adds to the first one's row, unscaled, in e5m2.
+// them adds to the first one's row, unscaled, in e5m2, which reaches down to 2^-16.
 template <int kParts, int kStack>
 __device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t* code) {
 #pragma unroll
@@ -628,9 +631,10 @@ __global__ void __launch_bounds__(384, 1)
     fa_cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const CacheParams p) {
   using L = CacheSmem<D, kBF16, R>;
-  constexpr int kStages = L::kStages, kParts = L::kParts, kStack = L::kStack, kPass = L::kPass;
-  constexpr int kSlots = 32 / R, kCopies = 8 * kSlots;  // copies per warp, in all (both warpgroups)
-  constexpr int kKeys = 32 * kStack / kSlots;           // keys per lane and tile: 16 or 32
+  constexpr int kStages = L::kStages, kStack = L::kStack, kQParts = L::kQParts, kPParts = L::kPParts;
+  constexpr int kQPass = L::kQPass, kPPass = L::kPPass;
+  constexpr int kCopies = 8 * (32 / R);  // of a row, in both warpgroups
+  constexpr int kKeys = R * kStack;      // keys whose weights a lane's row of P holds; the lane computes R of them
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(384, 1)
       auto issue_s = [&](int g) {
         const uint64_t b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kPass; ++q)
+        for (int q = 0; q < kQPass; ++q)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             umma_ss_f8(tmem + (g & 1) * 128, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
@@ -730,7 +734,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after_sync();
           const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
 #pragma unroll
-          for (int q = 0; q < kPass; ++q)
+          for (int q = 0; q < kPPass; ++q)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_ts_f8(tmem + 256 + (g & 1) * 128, tmem + (g & 1) * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
@@ -753,7 +757,8 @@ __global__ void __launch_bounds__(384, 1)
       const int wg = warp / 4, quarter = warp % 4;  // even or odd tiles; keys 32 * quarter .. + 31 of a tile
       const uint32_t lane_base = tmem + ((quarter * 32) << 16);
       const uint32_t s_tmem = lane_base + wg * 128, o_tmem = lane_base + 256 + wg * 128;
-      const int r = lane % R, stack = lane / R % kStack, share = lane / (R * kStack);  // row, part, share of the keys
+      // row; part (and which R of the row's kKeys keys this lane computes); which kKeys of the warp's 32 keys
+      const int r = lane % R, stack = lane / R % kStack, share = lane / kKeys;
       const float down = pow2i(-4 * stack);
       int joins = 0;
       auto join = [&]() {  // all threads of these warps, bounded like every wait
@@ -787,17 +792,17 @@ __global__ void __launch_bounds__(384, 1)
           if (piece == 0) row_back[row_q] = back * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
-            uint2 part[kPass * kStack];
-            q_split8<kBF16, kParts, kStack>(v[i], mul, part);
+            uint2 part[kQPass * kStack];
+            q_split8<kBF16, kQParts, kStack>(v[i], mul, part);
 #pragma unroll
-            for (int q = kParts; q < kPass * kStack; ++q) part[q] = make_uint2(0u, 0u);
+            for (int q = kQParts; q < kQPass * kStack; ++q) part[q] = make_uint2(0u, 0u);
             const int e8 = piece * kVec + i;  // 8-byte unit of the row
 #pragma unroll
             for (int c = 0; c < 128 / R; ++c) {
               const int m = c * R + row_q;
               uint8_t* dst = smem + L::kQOff + m * 128 + ((e8 >> 1) ^ (m & 7)) * 16 + (e8 & 1) * 8;
 #pragma unroll
-              for (int q = 0; q < kPass; ++q)
+              for (int q = 0; q < kQPass; ++q)
                 *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q * kStack + c % kStack];
             }
           }
@@ -821,37 +826,53 @@ __global__ void __launch_bounds__(384, 1)
         const int first = (wg - g) & 1;  // this warpgroup's first tile of the unit
         for (int it = first; it < left; it += 2) {
           const int gi = g + it, s = gi % kStages;
-          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * quarter + kKeys * share;
+          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * quarter + kKeys * share + R * stack;
           if (!mbar_wait(&s_full[wg], (gi >> 1) & 1, abort_flag) ||
               !mbar_wait(&k_full[s], (gi / kStages) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          float x[kKeys];
+          // Scores of this lane's R keys: the parts' partial scores of all kKeys keys lie in the kStack lanes of the row,
+          // which exchange halves until each has the sums of its own keys.
+          float x[R];
           {
             float v[32];
             tmem_ld_x32(s_tmem + 32 * quarter, reinterpret_cast<uint32_t*>(v));
+            if (kKeys == 16) {
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c) {
-              x[c] = (kKeys == 16 && share) ? v[(c + 16) % 32] : v[c];
-              if (kStack > 1) x[c] *= down;
-#pragma unroll
-              for (int o = R; o < R * kStack; o *= 2) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
+              for (int c = 0; c < 16; ++c) v[c] = share ? v[16 + c] : v[c];
             }
-          }
-          // this lane's 16-key groups: one or two
-          const float* f = fac + s * 24 + 2 * quarter + share;
-          const float a0 = c_row * f[0], lv0 = f[8], iv0 = f[16];
-          const float a1 = kKeys == 32 ? c_row * f[1] : a0, lv1 = kKeys == 32 ? f[9] : lv0;
-          const float iv1 = kKeys == 32 ? f[17] : iv0;
-          const bool masked = tile0 + 127 > t.c_min ||
-                              (p.win_left >= 0 && tile0 < t.c_max - p.win_left && tile0 + 127 >= p.sinks);
-          float mx = -INFINITY;
+            if (kStack > 1) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) {
-            x[c] = fmaf(x[c], c < 16 ? a0 : a1, c < 16 ? lv0 : lv1);
-            if (masked && (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks))) x[c] = -INFINITY;
-            mx = fmaxf(mx, x[c]);
+              for (int c = 0; c < kKeys; ++c) v[c] *= down;
+            }
+#pragma unroll
+            for (int n = kStack / 2; n > 0; n /= 2) {
+              const bool upper = (stack & n) != 0;
+#pragma unroll
+              for (int c = 0; c < R * n; ++c) {
+                const float keep = upper ? v[R * n + c] : v[c], send = upper ? v[c] : v[R * n + c];
+                v[c] = keep + __shfl_xor_sync(0xffffffffu, send, R * n);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < R; ++c) x[c] = v[c];
           }
-          const float m_new = fmaxf(m, mx);
+          // this lane's 16-key groups: one (R <= 16) or two
+          const float* f = fac + s * 24 + 2 * quarter + (kKeys * share + R * stack) / 16;
+          const float a0 = c_row * f[0], lv0 = f[8], iv0 = f[16];
+          const float a1 = R == 32 ? c_row * f[1] : a0, lv1 = R == 32 ? f[9] : lv0, iv1 = R == 32 ? f[17] : iv0;
+#pragma unroll
+          for (int c = 0; c < R; ++c) x[c] = fmaf(x[c], c < 16 ? a0 : a1, c < 16 ? lv0 : lv1);
+          if (tile0 + 127 > t.c_min ||
+              (p.win_left >= 0 && tile0 < t.c_max - p.win_left && tile0 + 127 >= p.sinks)) {
+#pragma unroll
+            for (int c = 0; c < R; ++c)
+              if (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks)) x[c] = -INFINITY;
+          }
+          float m_new = m;
+#pragma unroll
+          for (int c = 0; c < R; c += 2) m_new = fmax3(m_new, x[c], x[c + 1]);
+#pragma unroll
+          for (int n = 1; n < kStack; n *= 2) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, R * n));
           if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
             const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
             if (it >= 2) {
@@ -869,30 +890,63 @@ __global__ void __launch_bounds__(384, 1)
           }
           const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
           float sum0 = 0.f, sum1 = 0.f;
-          uint32_t pk[kPass][8];  // this warp's 32 keys of the row: this lane's part, zeros but for its own keys
+          uint32_t part[kPPass * kStack][R / 4];
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 4) {
+          for (int c = 0; c < R; c += 4) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[c + e] + off);
             (c < 16 ? sum0 : sum1) += (w[0] + w[1]) + (w[2] + w[3]);
-            uint32_t part[kPass * kStack];
-            p_split4<kParts, kStack>(w[0], w[1], w[2], w[3], part);
+            uint32_t code[kPParts];
+            p_split4<kPParts, kStack>(w[0], w[1], w[2], w[3], code);
 #pragma unroll
-            for (int q = kParts; q < kPass * kStack; ++q) part[q] = 0u;
+            for (int q = 0; q < kPPass * kStack; ++q) part[q][c / 4] = q < kPParts ? code[q] : 0u;
+          }
+          // The row of P in product q holds part q * kStack + stack of all kKeys keys: the same lanes exchange parts.
+          uint32_t pk[kPPass][8];  // this warp's 32 keys: zeros but for the lane's kKeys
 #pragma unroll
-            for (int q = 0; q < kPass; ++q) {
-              uint32_t mine = part[q * kStack];
+          for (int q = 0; q < kPPass; ++q) {
+            uint32_t row_p[kStack][R / 4];
 #pragma unroll
-              for (int k = 1; k < kStack; ++k) mine = k == stack ? part[q * kStack + k] : mine;
+            for (int u = 0; u < R / 4; ++u) {
+              if (kStack == 1) {
+                row_p[0][u] = part[q][u];
+              } else if (kStack == 2) {
+                const uint32_t keep = stack ? part[2 * q + 1][u] : part[2 * q][u];
+                const uint32_t send = stack ? part[2 * q][u] : part[2 * q + 1][u];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, R);
+                row_p[0][u] = stack ? got : keep;
+                row_p[kStack - 1][u] = stack ? keep : got;
+              } else {
+                const bool hi = (stack & 2) != 0, lo = (stack & 1) != 0;
+                uint32_t half[2][2];  // [part within this lane's pair][keys of the lower, upper two lanes]
 #pragma unroll
-              for (int k = 0; k < 32 / kKeys; ++k) pk[q][k * (kKeys / 4) + c / 4] = k == share ? mine : 0u;
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t keep = hi ? part[(2 + k) % (kPPass * kStack)][u] : part[k][u];
+                  const uint32_t send = hi ? part[k][u] : part[(2 + k) % (kPPass * kStack)][u];
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 2 * R);
+                  half[k][0] = hi ? got : keep;
+                  half[k][1] = hi ? keep : got;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t keep = lo ? half[1][k] : half[0][k], send = lo ? half[0][k] : half[1][k];
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, send, R);
+                  row_p[(2 * k) % kStack][u] = lo ? got : keep;
+                  row_p[(2 * k + 1) % kStack][u] = lo ? keep : got;
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t own = row_p[k * 4 / R % kStack][k % (R / 4)];
+              pk[q][k] = (kKeys == 32 || k / 4 == share) ? own : 0u;
             }
           }
           l += sum0 * iv0 + sum1 * iv1;
           const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int q = 0; q < kPass; ++q)
+          for (int q = 0; q < kPPass; ++q)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t at = s_tmem + q * 32 + 8 * k;
@@ -924,7 +978,7 @@ __global__ void __launch_bounds__(384, 1)
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
 #pragma unroll
         for (int q = 0; q < kCopies; ++q)
-          if (q % kStack == 0) l_all += q_l[q * R + r] * ex2_approx(q_m[q * R + r] - m_use);
+          l_all += q_l[q * R + r] * ex2_approx(q_m[q * R + r] - m_use);
         float f = ex2_approx(m - m_use) * down;
         if (whole) f *= l_all == 0.f ? 0.f : 1.f / l_all;  // l = 0: no visible key (a NaN stays one)
         const size_t slot0 = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * R;
@@ -988,7 +1042,7 @@ __global__ void __launch_bounds__(384, 1)
                          const CacheParams p) {
   constexpr int kRows = 256;
   using L = CacheSmem<D, kBF16, kRows>;
-  constexpr int kStages = L::kStages, kParts = L::kParts;
+  constexpr int kStages = L::kStages, kQParts = L::kQParts, kPParts = L::kPParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -1055,7 +1109,7 @@ __global__ void __launch_bounds__(384, 1)
       auto issue_s = [&](int t, int g) {
         const uint64_t a0 = sdesc_add(q_desc, t * L::kTile), b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+        for (int q = 0; q < kQParts; ++q)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             umma_ss_f8(tmem + t * 128, sdesc_add(a0, q * 2 * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
@@ -1066,7 +1120,7 @@ __global__ void __launch_bounds__(384, 1)
       auto issue_o = [&](int t, int g, bool acc, int half) {
         const uint64_t b0 = sdesc_add(v_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+        for (int q = 0; q < kPParts; ++q)
 #pragma unroll
           for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
             umma_ts_f8(tmem + 256 + t * 128, tmem + t * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
@@ -1157,11 +1211,11 @@ __global__ void __launch_bounds__(384, 1)
         c_row = back * p.scale_log2;
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
-          uint2 part[kParts];
-          q_split8<kBF16, kParts, 1>(src[i], mul, part);
+          uint2 part[kQParts];
+          q_split8<kBF16, kQParts, 1>(src[i], mul, part);
           uint8_t* dst = smem + L::kQOff + t * L::kTile + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kTile) = part[q];
+          for (int q = 0; q < kQParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kTile) = part[q];
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_ready[t]);
@@ -1223,7 +1277,7 @@ __global__ void __launch_bounds__(384, 1)
         float lsum = 0.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[kParts][16];
+          uint32_t pk[kPParts][16];
 #pragma unroll
           for (int gr = 4 * half; gr < 4 * half + 4; ++gr) {
             uint64_t sum2 = f2_pack(0.f, 0.f);
@@ -1237,17 +1291,17 @@ __global__ void __launch_bounds__(384, 1)
               w2_ = ex2_approx(w2_);
               w3_ = ex2_approx(w3_);
               sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
-              uint32_t part[kParts];
-              p_split4<kParts, 1>(w0_, w1_, w2_, w3_, part);
+              uint32_t part[kPParts];
+              p_split4<kPParts, 1>(w0_, w1_, w2_, w3_, part);
 #pragma unroll
-              for (int q = 0; q < kParts; ++q) pk[q][(c - 64 * half) / 4] = part[q];
+              for (int q = 0; q < kPParts; ++q) pk[q][(c - 64 * half) / 4] = part[q];
             }
             float s0, s1;
             f2_unpack(sum2, s0, s1);
             lsum = fmaf(s0 + s1, f[16 + gr], lsum);
           }
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) tmem_st_x16(s_tmem + q * 32 + half * 16, pk[q]);
+          for (int q = 0; q < kPParts; ++q) tmem_st_x16(s_tmem + q * 32 + half * 16, pk[q]);
           tmem_st_wait();
           tc_fence_before_sync();
           mbar_arrive(half ? &p_full[t] : &p_half[t]);
