@@ -23,9 +23,9 @@
 // Scales lie in [2^-50, 2^50], so l (at most 2^(6+2+100) times the number of keys) stays finite.
 //
 // Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
-// tiles, and before them the tiles with sinks). All units' tiles are laid end to end and every CTA takes an equal
-// run of them, whatever the lengths are, so a batch with one long sequence loads the SMs evenly. Units cut by a
-// run's border leave fp32 partial sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so
+// tiles, and before them the tiles with sinks). All units' tiles are laid end to end, each unit's with a few places
+// before them for what a unit costs by itself (kCacheUnitCost), and every CTA takes an equal run of places, whatever the
+// lengths are, so neither one long sequence nor many short ones load the SMs unevenly. Units cut by a run's border leave fp32 partial sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so
 // results repeat bit for bit.
 #pragma once
 #include "fa_fwd.cuh"
@@ -33,6 +33,8 @@
 namespace fa {
 
 constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that the workspace size needs no device
+// Beginning and ending a unit takes a CTA about as long as this many tiles.
+constexpr int kCacheUnitCost = 3;
 constexpr float kCacheLag = 2.0f;    // how far the running maximum may lag (log2)
 constexpr float kCacheShift = 6.0f;  // weights carry 2^6 (see above)
 
@@ -267,65 +269,93 @@ struct CacheRun {
   int count;     // tiles of this CTA
   CachePos first;
 };
+struct CacheScan {  // shared memory of cache_run
+  long long sums[12][2];
+  long long begin_tile, end_tile;  // tiles before the run's two ends
+  CachePos first;
+};
 
-// This CTA's run of tiles, found by every thread together (kThreads of them): all items' tiles are counted, then the
-// item holding the run's first tile is searched. Also notes the unit cut there, for the join.
+// This CTA's run of tiles, found by every thread together (kThreads of them). Places: a unit of n tiles takes
+// kCacheUnitCost + n of them, its tiles the last n; CTA c takes places [c share, (c + 1) share). All items are counted
+// first, then those holding the run's two ends are searched. Also notes the unit cut at the run's begin, for the join.
 template <int kRows, int kThreads>
-__device__ __forceinline__ CacheRun cache_run(const CacheParams& p, long long* scratch /* kThreads / 32 + 1 */,
-                                              CacheRun* shared) {
+__device__ __forceinline__ CacheRun cache_run(const CacheParams& p, CacheScan* sh) {
   const int items = p.B * p.n_mt, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
-  long long sum = 0;
-  for (int x = tid; x < items; x += kThreads) sum += cache_item<kRows>(p, x).n;
+  long long tiles = 0;
+  for (int x = tid; x < items; x += kThreads) tiles += cache_item<kRows>(p, x).n;
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  if (lane == 0) scratch[warp] = sum;
-  if (tid == 0) shared->count = 0;
-  __syncthreads();
-  long long total = 0;
-  for (int i = 0; i < kWarps; ++i) total += scratch[i];
-  total *= p.Hkv;
-  const long long share = (total + kCacheCtas - 1) / kCacheCtas;
-  const long long begin = share * blockIdx.x, end = min(begin + share, total);
-  if (begin < end) {
-    long long base = 0;
-    for (int x0 = 0; x0 < items; x0 += kThreads) {
-      const int x = x0 + tid;
-      const int n = x < items ? cache_item<kRows>(p, x).n : 0;
-      const long long mine = static_cast<long long>(n) * p.Hkv;
-      long long incl = mine;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += o;
-      }
-      __syncthreads();
-      if (lane == 31) scratch[warp] = incl;
-      __syncthreads();
-      long long before = base;
-      for (int i = 0; i < warp; ++i) before += scratch[i];
-      const long long lo = before + incl - mine, hi = before + incl;
-      if (lo <= begin && begin < hi) {
-        const long long rel = begin - lo;
-        CacheRun r;
-        r.count = static_cast<int>(end - begin);
-        r.first = {x, static_cast<int>(rel / n), static_cast<int>(rel % n)};
-        *shared = r;
-        // The unit holding the tile before: cut at `begin` if it goes on here; its first CTA's successor joins it.
-        int4 cut = make_int4(-1, 0, 0, 0);
-        const long long u0 = begin - r.first.w;
-        if (r.first.w > 0 && u0 / share == blockIdx.x - 1)
-          cut = make_int4(x, r.first.hk, static_cast<int>((u0 + n - 1) / share), 0);
-        p.cuts[blockIdx.x] = cut;
-      }
-      for (int i = 0; i < kWarps; ++i) base += scratch[i];
-      if (begin < base) break;
-    }
-  } else if (tid == 0) {
+  for (int s = 16; s > 0; s >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, s);
+  if (lane == 0) sh->sums[warp][0] = tiles;
+  if (tid == 0) {
+    sh->begin_tile = sh->end_tile = 0;
     p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   __syncthreads();
-  return *shared;
+  long long total_tiles = 0;
+  for (int i = 0; i < kWarps; ++i) total_tiles += sh->sums[i][0];
+  total_tiles *= p.Hkv;
+  const long long total = total_tiles + static_cast<long long>(items) * p.Hkv * kCacheUnitCost;
+  const long long share = (total + kCacheCtas - 1) / kCacheCtas;
+  const long long begin = share * blockIdx.x, end = begin + share;
+  if (begin < total) {  // (uniform)
+    if (tid == 0 && end >= total) sh->end_tile = total_tiles;
+    long long place = 0, tile = 0;  // of the first item of the chunk
+    for (int x0 = 0; x0 < items; x0 += kThreads) {
+      const int x = x0 + tid;
+      const int n = x < items ? cache_item<kRows>(p, x).n : 0;
+      const long long my_tiles = static_cast<long long>(n) * p.Hkv;
+      const long long mine = x < items ? my_tiles + static_cast<long long>(p.Hkv) * kCacheUnitCost : 0;
+      long long incl = mine, incl_t = my_tiles;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, s), ot = __shfl_up_sync(0xffffffffu, incl_t, s);
+        if (lane >= s) {
+          incl += o;
+          incl_t += ot;
+        }
+      }
+      __syncthreads();  // the sums of the count, or of the chunk before, are read
+      if (lane == 31) {
+        sh->sums[warp][0] = incl;
+        sh->sums[warp][1] = incl_t;
+      }
+      __syncthreads();
+      long long lo = place + incl - mine, lo_t = tile + incl_t - my_tiles;
+      for (int i = 0; i < warp; ++i) {
+        lo += sh->sums[i][0];
+        lo_t += sh->sums[i][1];
+      }
+      // The first tile at or after place `at` of this thread's item, and how many tiles come before it.
+      auto find = [&](long long at, CachePos* pos) {
+        const long long rel = at - lo, unit = n + kCacheUnitCost;
+        pos->x = x;
+        pos->hk = static_cast<int>(rel / unit);
+        pos->w = max(0, static_cast<int>(rel % unit) - kCacheUnitCost);
+        return lo_t + static_cast<long long>(pos->hk) * n + pos->w;
+      };
+      if (lo <= begin && begin < lo + mine) {
+        CachePos first;
+        sh->begin_tile = find(begin, &first);
+        sh->first = first;
+        // A unit that goes on here: its first piece's successor joins it.
+        const long long u0 = begin - first.w;  // its first tile's place
+        if (first.w > 0 && u0 / share == blockIdx.x - 1)
+          p.cuts[blockIdx.x] = make_int4(x, first.hk, static_cast<int>((u0 + n - 1) / share), 0);
+      }
+      if (lo <= end && end < lo + mine) {
+        CachePos last;
+        sh->end_tile = find(end, &last);
+      }
+      for (int i = 0; i < kWarps; ++i) {
+        place += sh->sums[i][0];
+        tile += sh->sums[i][1];
+      }
+      if (end < place) break;
+    }
+  }
+  __syncthreads();
+  return {static_cast<int>(sh->end_tile - sh->begin_tile), sh->first};
 }
 
 // Where a piece of a unit leaves its sums: slot 0 of its CTA if the unit began before, slot 1 if it goes on after.
@@ -389,16 +419,17 @@ struct CacheSmem {
   static constexpr int kQOff = 0;                    // [product][Q tile]
   static constexpr int kKOff = kQOff + kQPass * kNQ * kTile;
   static constexpr int kVOff = kKOff + kStages * kTile;
-  static constexpr int kXOff = kVOff + kStages * kTile;  // kFew: 32 columns of all copies' O, 256 lanes x 33 floats
-  static constexpr int kXBytes = kFew ? 256 * 33 * 4 : 0;
+  // kFew: kJoinCols columns of the warps' O, [8 warps][R rows][kJoinCols + 4] floats
+  static constexpr int kJoinCols = kFew ? (1024 / R < D ? 1024 / R : D) : 0;
+  static constexpr int kXOff = kVOff + kStages * kTile;
+  static constexpr int kXBytes = kFew ? 8 * R * (kJoinCols + 4) * 4 : 0;
   static constexpr int kFacOff = kXOff + kXBytes;    // per stage: k factor, log2 v scale, 1 / v scale of 8 key groups
   static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per lane [2][256]
   static constexpr int kMlBytes = kFew ? (32 + 512) * 4 : 0;
   static constexpr int kBarOff = kMlOff + kMlBytes;
   static constexpr int kNumBars = 4 * kStages + 11;
-  static constexpr int kRunOff = kBarOff + kNumBars * 8;
-  static constexpr int kScanOff = kRunOff + 16;
-  static constexpr int kMiscOff = kScanOff + 13 * 8;
+  static constexpr int kScanOff = kBarOff + kNumBars * 8;
+  static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
   static constexpr int kThreads = 384;
   static constexpr uint32_t kTmemCols = 512;
@@ -470,6 +501,13 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
         ok = false;
         break;
       }
+      // The copies need the page number only; their bytes count towards a phase that the arrival below opens and ends.
+      if (tt == u && leads) {
+        const int row = cur.row >= 0 ? cur.row : beyond;
+        tma_load_2d(smem_k + s * 16384 + grp * 2048, &tm_k, &k_full[s], 0, row);
+        tma_load_2d(smem_v + s * 16384 + grp * 2048, &tm_v, &v_full[s], 0, row);
+      }
+      __syncwarp();
       if (tt == u) {
         const bool valid = cur.row >= 0;
         fac[s * 24 + grp] = valid ? cur.ks : 0.f;
@@ -481,13 +519,6 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
         mbar_arrive_expect_tx(&k_full[s], 16384);
         mbar_arrive_expect_tx(&v_full[s], 16384);
       }
-      __syncwarp();
-      if (tt == u && leads) {
-        const int row = cur.row >= 0 ? cur.row : beyond;
-        tma_load_2d(smem_k + s * 16384 + grp * 2048, &tm_k, &k_full[s], 0, row);
-        tma_load_2d(smem_v + s * 16384 + grp * 2048, &tm_v, &v_full[s], 0, row);
-      }
-      __syncwarp();
     }
     cur = nxt;
     nxt = far;
@@ -682,8 +713,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  const CacheRun run = cache_run<R, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
-                                                 reinterpret_cast<CacheRun*>(smem + L::kRunOff));
+  const CacheRun run = cache_run<R, L::kThreads>(p, reinterpret_cast<CacheScan*>(smem + L::kScanOff));
   if (warp >= 8) {
     regs_dec<88>();
     if (run.count == 0) {
@@ -765,13 +795,13 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(joint);
         return mbar_wait(joint, joins++ & 1, abort_flag);
       };
-      // q of a unit into the A operand, each row to its 128 / R places. The previous unit's scores must be complete.
+      // q of a unit: from memory to registers (ahead of time), and from there into the A operand, each row to its 128 / R
+      // places, when the previous unit's scores are complete.
+      constexpr int kVec = D * R > 256 * 8 ? D * R / (256 * 8) : 1;  // 8-element vectors per thread
+      constexpr int kThreadsPerRow = D / (8 * kVec);
+      const int row_q = threadIdx.x / kThreadsPerRow, piece = threadIdx.x % kThreadsPerRow;
+      uint4 v[kVec];
       auto load_q = [&](const CacheItem& t, int hk) {
-        constexpr int kVec = D * R > 256 * 8 ? D * R / (256 * 8) : 1;  // 8-element vectors per thread
-        constexpr int kThreadsPerRow = D / (8 * kVec);
-        const int row_q = threadIdx.x / kThreadsPerRow, piece = threadIdx.x % kThreadsPerRow;
-        uint4 v[kVec];
-        uint32_t amax = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row_q < t.rows) {
@@ -781,9 +811,12 @@ __global__ void __launch_bounds__(384, 1)
                              piece * kVec;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) v[i] = src[i];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
         }
+      };
+      auto place_q = [&]() {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
 #pragma unroll
         for (int s = 1; s < kThreadsPerRow; s <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, s));
         float mul, back;
@@ -813,6 +846,7 @@ __global__ void __launch_bounds__(384, 1)
       CacheWalk<R> walk;
       walk.start(p, run.first);
       load_q(walk.item, walk.at.hk);
+      place_q();
       bool ok = join();
       for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
         const CacheItem t = walk.item;
@@ -822,6 +856,11 @@ __global__ void __launch_bounds__(384, 1)
         const int row = t.row0 + min(r, t.rows - 1);
         const int aligned = t.c0 + row / p.group;
         const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
+        const bool more = g + left < run.count;
+        if (more) {  // while the first scores are on their way
+          walk.advance(p, left);
+          load_q(walk.item, walk.at.hk);
+        }
         float m = -INFINITY, l = 0.f;
         const int first = (wg - g) & 1;  // this warpgroup's first tile of the unit
         for (int it = first; it < left; it += 2) {
@@ -964,12 +1003,11 @@ __global__ void __launch_bounds__(384, 1)
         // ---- the unit's (or piece's) end. The next unit's q first: its scores can run during the join.
         q_m[warp * 32 + lane] = m;
         q_l[warp * 32 + lane] = l;
-        const bool whole = left == t.n, more = g < run.count;
+        const bool whole = left == t.n;
         if (more) {
           // (the last tile's scores may be the other warpgroup's)
           if (!mbar_wait(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
-          walk.advance(p, left);
-          load_q(walk.item, walk.at.hk);
+          place_q();
         }
         if (!join()) { ok = false; break; }
         float m_all = -INFINITY, l_all = 0.f;
@@ -993,30 +1031,57 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (!mbar_wait(unit_done, unit & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
+        // O: first the copies within a warp (the lanes of a row exchange halves of 32 columns until each has the sums of
+        // R), then the warps, through shared memory.
         float* xo = reinterpret_cast<float*>(smem + L::kXOff);
+        constexpr int kCols = L::kJoinCols, kStride = kCols + 4;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-          // (A copy that saw no key of this row has f = 0, and weights 0: its O is 0. A warpgroup without a tile in
-          // this unit has no O at all.)
+        for (int cb = 0; cb < D; cb += kCols) {
+          if (cb > 0 && !join()) { ok = false; break; }
+#pragma unroll 1
+          for (int c0 = 0; c0 < kCols; c0 += 32) {
+            float o[32];
+            tmem_ld_x32(o_tmem + cb + c0, reinterpret_cast<uint32_t*>(o));
+            // (A copy that saw no key of this row has f = 0, and weights 0: its O is 0. A warpgroup without a tile in
+            // this unit has no O at all.)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) xo[(warp * 32 + lane) * 33 + c] = first < left ? o[c] * f : 0.f;
-          if (!join()) { ok = false; break; }
-          for (int ro = warp; ro < t.rows; ro += 8) {
-            float v = 0.f;
+            for (int c = 0; c < 32; ++c) o[c] = first < left ? o[c] * f : 0.f;
 #pragma unroll
-            for (int q = 0; q < kCopies; ++q) v += xo[(q * R + ro) * 33 + lane];
-            if (whole) {
-              const int rr = t.row0 + ro, qi = rr / p.group, h = hk * p.group + rr % p.group;
-              static_cast<uint16_t*>(p.out)[((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + c0 + lane] =
-                  static_cast<uint16_t>(pack2<kBF16>(v, 0.f));
-            } else {
-              p.part_o[(slot0 + ro) * D + c0 + lane] = v;
+            for (int n = 16 / R; n > 0; n /= 2) {
+              const bool upper = (lane / R & n) != 0;
+#pragma unroll
+              for (int c = 0; c < R * n; ++c) {
+                const float keep = upper ? o[R * n + c] : o[c], send = upper ? o[c] : o[R * n + c];
+                o[c] = keep + __shfl_xor_sync(0xffffffffu, send, R * n);
+              }
             }
+            float* dst = xo + (warp * R + r) * kStride + c0 + (lane / R) * R;
+#pragma unroll
+            for (int c = 0; c < R; c += 4)
+              *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
           }
           if (!join()) { ok = false; break; }
+          const int ro = threadIdx.x / (kCols / 4), col = threadIdx.x % (kCols / 4) * 4;
+          if (ro < t.rows) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const float4 x = *reinterpret_cast<const float4*>(xo + (w * R + ro) * kStride + col);
+              sum.x += x.x;
+              sum.y += x.y;
+              sum.z += x.z;
+              sum.w += x.w;
+            }
+            if (whole) {
+              const int rr = t.row0 + ro, qi = rr / p.group, h = hk * p.group + rr % p.group;
+              uint16_t* dst = static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + cb + col;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kBF16>(sum.x, sum.y), pack2<kBF16>(sum.z, sum.w));
+            } else {
+              *reinterpret_cast<float4*>(p.part_o + (slot0 + ro) * D + cb + col) = sum;
+            }
+          }
         }
+        if (!ok) break;
         tc_fence_before_sync();
       }
     }
@@ -1087,8 +1152,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<long long*>(smem + L::kScanOff),
-                                                     reinterpret_cast<CacheRun*>(smem + L::kRunOff));
+  const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<CacheScan*>(smem + L::kScanOff));
   if (warp >= 8) {
     regs_dec<88>();
     if (run.count == 0) {
