@@ -19,6 +19,7 @@ Every operand (inputs and caller-passed outputs alike) is checked against these 
 device of ``q`` before anything is launched; a mismatch raises ``ValueError`` or ``TypeError``. Each call
 runs with ``q``'s device current and, unless a stream is given, on that device's current stream.
 """
+import contextlib
 import ctypes
 import os
 
@@ -112,6 +113,9 @@ def _dtype_code(t):
 def _check(name, t, dev, shape=None, dtype=None):
     """``t`` must be a contiguous tensor on the CUDA device ``dev`` (and have ``shape`` / ``dtype`` if given)."""
     d = getattr(t, "device", None)
+    if (d == dev and t.is_contiguous() and (shape is None or t.shape == shape)
+            and (dtype is None or t.dtype == dtype) and d.type == "cuda"):
+        return
     if d is None or d.type != "cuda" or d != dev:
         raise ValueError("%s must be a CUDA tensor on %s, got %s" % (name, dev, d))
     if not t.is_contiguous():
@@ -200,15 +204,18 @@ def _used_on(stream, *tensors):
 def _stream(stream, dev):
     import torch
 
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError("stream is on %s but the tensors are on %s" % (s.device, dev))
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError("stream is on %s but the tensors are on %s" % (stream.device, dev))
+    return stream.cuda_stream
 
 
 def _device(dev):
     import torch
 
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
     return torch.cuda.device(dev)
 
 

@@ -4,7 +4,7 @@
 // K and for V (value = code * scale); a table [B, max_pages] of page numbers and a length per sequence. A page of one
 // head is contiguous (page * D bytes), so it arrives as one TMA box, and 128 keys of a head are 128 / page boxes.
 //
-// Attention without converting the cache. K and V stay e4m3 all the way into the tensor core (tcgen05 kind::f8f6f4);
+// Few query rows (decoding): attention without converting the cache. K and V stay e4m3 all the way into the tensor core (tcgen05 kind::f8f6f4);
 // it is the other operand that is brought to 8 bits, without loss: a 16-bit number has 8 (bf16) or 11 (fp16)
 // significant bits and an e4m3 number 4, so q = q1 + q2 (+ q3) with q1 = e4m3(q), q2 = e4m3(q - q1) and, for fp16,
 // a third part for the 3 bits left is exact as long as the parts stay in range (split_f16x2).
@@ -37,11 +37,15 @@ constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that 
 constexpr int kCacheUnitCost = 3;
 constexpr float kCacheLag = 2.0f;    // how far the running maximum may lag (log2)
 constexpr float kCacheShift = 6.0f;  // weights carry 2^6 (see above)
+// The same for blocks of many rows, whose weights are fp16 (w <= 2^15; what is lost lies below 2^-34 of the largest).
+constexpr float kManyLag = 6.0f, kManyShift = 9.0f;
 
 struct CacheParams {
   const void* q;         // [B, Sq, H, D]
   void* out;             // [B, Sq, H, D]
   float* lse;            // [B, H, Sq]
+  const uint8_t* k_pages;  // [num_pages, Hkv, page, D] (read through tensor maps for few rows)
+  const uint8_t* v_pages;
   const float* k_scale;  // [num_pages, Hkv]
   const float* v_scale;
   const int* table;      // [B, max_pages]
@@ -53,6 +57,7 @@ struct CacheParams {
   int n_rows, n_mt;      // query rows of a (sequence, K/V head) = Sq * group; units they make
   int page, max_pages, num_pages;
   int win_left, sinks;   // win_left < 0: no window (sinks = 0 then)
+  int whole;             // units are not cut (all are short): no join follows
   float scale_log2;
 };
 
@@ -270,7 +275,7 @@ struct CacheRun {
   CachePos first;
 };
 struct CacheScan {  // shared memory of cache_run
-  long long sums[12][2];
+  long long sums[16][2];
   long long begin_tile, end_tile;  // tiles before the run's two ends
   CachePos first;
 };
@@ -326,13 +331,15 @@ __device__ __forceinline__ CacheRun cache_run(const CacheParams& p, CacheScan* s
         lo += sh->sums[i][0];
         lo_t += sh->sums[i][1];
       }
-      // The first tile at or after place `at` of this thread's item, and how many tiles come before it.
+      // The first tile at or after place `at` of this thread's item (of a unit that begins there, if units stay
+      // whole), and how many tiles come before it.
       auto find = [&](long long at, CachePos* pos) {
-        const long long rel = at - lo, unit = n + kCacheUnitCost;
-        pos->x = x;
-        pos->hk = static_cast<int>(rel / unit);
-        pos->w = max(0, static_cast<int>(rel % unit) - kCacheUnitCost);
-        return lo_t + static_cast<long long>(pos->hk) * n + pos->w;
+        const long long unit = n + kCacheUnitCost, rel = at - lo + (p.whole ? unit - 1 : 0);
+        const int hk = static_cast<int>(rel / unit);
+        pos->x = hk < p.Hkv ? x : x + 1;
+        pos->hk = hk < p.Hkv ? hk : 0;
+        pos->w = p.whole ? 0 : max(0, static_cast<int>(rel % unit) - kCacheUnitCost);
+        return lo_t + static_cast<long long>(hk) * n + pos->w;
       };
       if (lo <= begin && begin < lo + mine) {
         CachePos first;
@@ -396,38 +403,35 @@ __global__ void __launch_bounds__(256) fa_cache_join_kernel(const CacheParams p)
         make_uint2(pack2<kBF16>(o.x * inv, o.y * inv), pack2<kBF16>(o.z * inv, o.w * inv));
     if (d == 0)
       p.lse[(static_cast<size_t>(t.b) * p.H + h) * p.Sq + i] =
-          l == 0.f ? -INFINITY : (m + log2f(l) - kCacheShift) * kLn2;
+          l == 0.f ? -INFINITY : (m + log2f(l) - (kRows == 256 ? kManyShift : kCacheShift)) * kLn2;
   }
 }
 
 // --------------------------------------------------------------------------------------------- shared pieces
 constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A in e5m2 (B in e4m3)
 
-// R: query rows per unit: 8, 16 or 32 (decoding), or blocks of 256 (chunks of prompts).
+// Few query rows per unit: R = 8, 16 or 32.
 template <int D, bool kBF16, int R>
 struct CacheSmem {
-  static constexpr bool kFew = R <= 32;
-  static constexpr int kNQ = kFew ? 1 : 2;           // 128-row Q tiles
-  // Parts of q and of the weights. Few rows: the A operand holds every row 128 / R times, kStack of them with different
-  // parts. Where the parts are not stacked (and so not scaled) the weights get a third one for the sake of small weights.
+  // Parts of q and of the weights. The A operand holds every row 128 / R times, kStack of them with different parts.
+  // Where the parts are not stacked (and so not scaled) the weights get a third one for the sake of small weights.
   static constexpr int kStack = R == 8 ? (kBF16 ? 2 : 4) : R == 16 ? 2 : 1;
   static constexpr int kQParts = kBF16 ? 2 : 3, kPParts = kBF16 && kStack > 1 ? 2 : 3;
   static constexpr int kQPass = (kQParts + kStack - 1) / kStack;  // products per S
   static constexpr int kPPass = (kPParts + kStack - 1) / kStack;  // products per O
   static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
-  static constexpr int kStages = kFew && kQPass == 1 ? 5 : 4;
-  static constexpr int kQOff = 0;                    // [product][Q tile]
-  static constexpr int kKOff = kQOff + kQPass * kNQ * kTile;
+  static constexpr int kStages = kQPass == 1 ? 5 : 4;
+  static constexpr int kQOff = 0;                    // [product]
+  static constexpr int kKOff = kQOff + kQPass * kTile;
   static constexpr int kVOff = kKOff + kStages * kTile;
-  // kFew: kJoinCols columns of the warps' O, [8 warps][R rows][kJoinCols + 4] floats
-  static constexpr int kJoinCols = kFew ? (1024 / R < D ? 1024 / R : D) : 0;
+  // kJoinCols columns of the warps' O, [8 warps][R rows][kJoinCols + 4] floats
+  static constexpr int kJoinCols = 1024 / R < D ? 1024 / R : D;
   static constexpr int kXOff = kVOff + kStages * kTile;
-  static constexpr int kXBytes = kFew ? 8 * R * (kJoinCols + 4) * 4 : 0;
+  static constexpr int kXBytes = 8 * R * (kJoinCols + 4) * 4;
   static constexpr int kFacOff = kXOff + kXBytes;    // per stage: k factor, log2 v scale, 1 / v scale of 8 key groups
-  static constexpr int kMlOff = kFacOff + kStages * 96;  // kFew: row factors [32], m and l per lane [2][256]
-  static constexpr int kMlBytes = kFew ? (32 + 512) * 4 : 0;
-  static constexpr int kBarOff = kMlOff + kMlBytes;
-  static constexpr int kNumBars = 4 * kStages + 11;
+  static constexpr int kMlOff = kFacOff + kStages * 96;  // row factors [32], m and l per lane [2][256]
+  static constexpr int kBarOff = kMlOff + (32 + 512) * 4;
+  static constexpr int kNumBars = 4 * kStages + 8;
   static constexpr int kScanOff = kBarOff + kNumBars * 8;
   static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
@@ -649,7 +653,7 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 // warp has 32, and where copies are left its lanes take 16 each; a copy has a running maximum, sum and rows of O of its
 // own, and weights of 0 for the others' keys. Nothing else is exchanged until the copies are joined, once, at the end of
 // the unit. (One product with all parts instead of one per part: 32 x 32768 tokens, 64 query heads on 8, bf16:
-// 505 -> TODO us; an M = N = 128, K = 32 product of 8-bit operands takes 115 to 140 cycles here, so the products were the bound.)
+// 505 -> 427 us; an M = N = 128, K = 32 product of 8-bit operands takes 115 to 140 cycles here, so the products were the bound.)
 //
 // Warps: 0-3 and 4-7 softmax of the even and the odd tiles of the run, each warpgroup with its own S and O (so its own
 // maxima and sums too, joined with the others at the end): two tiles are in work at any time, and a warpgroup's
@@ -1096,26 +1100,44 @@ __global__ void __launch_bounds__(384, 1)
 
 // ------------------------------------------------------------------------------- attention of many query rows
 // Chunks of prompts: units of 256 rows (two 128-row Q tiles, each with its own softmax warpgroup, thread = row), as in
-// the forward of fa_fwd.cuh: while one warpgroup runs the softmax of its tile the tensor core works on the other.
-// Bound by the tensor core (2 or 3 e4m3 products for each of S and O) and the exponentials.
+// the forward of fa_fwd.cuh: while one warpgroup runs the softmax of its tile the tensor core works on the other. With
+// this many rows a key is used often enough that converting it once is cheaper than splitting every weight into 8-bit
+// parts: a converting warpgroup reads the pages (prefetched in registers), and writes K and V as fp16 (exact) into the
+// shared-memory tiles of the 16-bit products; q enters as fp16 scaled per row (exact, as above), the weights in one
+// fp16 rounding. (Splitting measured 788 us where this takes TODO: 4096 tokens of a prompt of 8192, 32 heads on 8, bf16;
+// its conversions to e4m3 run at a quarter of the rate of other arithmetic.) Rows that no query sees are written as 0.
 //
-// Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8 TMA, 9 MMA, 10 cleaner, 11 idle. TMEM columns: S0 [0,128),
-// S1 [128,256), O0 [256,384), O1 [384,512); the parts of P_t overwrite S_t, 32 columns each.
+// Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8-11 conversion, 12 MMA, 13-15 idle. TMEM columns: S0 [0,128),
+// S1 [128,256), O0 [256,256+D), O1 [384,384+D); P_t overwrites the first 64 columns of S_t.
+template <int D>
+struct CacheManySmem {
+  static constexpr int kRows = 256, kStages = 2;
+  static constexpr int kTile = 128 * D * 2;           // 128 rows of fp16: D / 64 chunks of 128-byte swizzle rows
+  static constexpr int kQOff = 0;                     // [Q tile]
+  static constexpr int kKOff = kQOff + 2 * kTile;
+  static constexpr int kVOff = kKOff + kStages * kTile;
+  static constexpr int kFacOff = kVOff + kStages * kTile;
+  static constexpr int kBarOff = kFacOff + kStages * 96;
+  static constexpr int kNumBars = 3 * kStages + 11;
+  static constexpr int kScanOff = kBarOff + kNumBars * 8;
+  static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
+  static constexpr int kAlloc = kMiscOff + 16 + 1024;
+  static constexpr int kThreads = 512;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(384, 1)
-    fa_cache_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const CacheParams p) {
-  constexpr int kRows = 256;
-  using L = CacheSmem<D, kBF16, kRows>;
-  constexpr int kStages = L::kStages, kQParts = L::kQParts, kPParts = L::kPParts;
+__global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams p) {
+  using L = CacheManySmem<D>;
+  constexpr int kStages = L::kStages, kRows = L::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint64_t* k_full = bars;
-  uint64_t* v_full = k_full + kStages;
-  uint64_t* kv_empty = v_full + kStages;
-  uint64_t* v_clean = kv_empty + kStages;
-  uint64_t* s_full = v_clean + kStages;   // [2]
+  uint64_t* k_full = bars;                // [kStages]
+  uint64_t* v_full = k_full + kStages;    // [kStages]
+  uint64_t* kv_empty = v_full + kStages;  // [kStages]
+  uint64_t* s_full = kv_empty + kStages;  // [2]
   uint64_t* p_half = s_full + 2;          // [2] weights of keys 0..63 published
   uint64_t* p_full = s_full + 4;          // [2]
   uint64_t* o_full = s_full + 6;          // [2]
@@ -1128,10 +1150,9 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&v_full[s], 1);
+      mbar_init(&k_full[s], 128);
+      mbar_init(&v_full[s], 128);
       mbar_init(&kv_empty[s], 1);
-      mbar_init(&v_clean[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -1144,7 +1165,7 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 12) {
     tmem_alloc(tmem_holder, L::kTmemCols);
     tmem_relinquish();
   }
@@ -1153,43 +1174,29 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
   const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<CacheScan*>(smem + L::kScanOff));
-  if (warp >= 8) {
-    regs_dec<88>();
-    if (run.count == 0) {
-    } else if (warp == 8) {
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-      }
-      cache_producer<kRows, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
-                                     kv_empty, abort_flag);
-    } else if (warp == 9 && lane == 0) {
+  if (warp >= 12) {
+    if (warp == 12 && lane == 0 && run.count > 0) {
       // ---------------------------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
-      constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
+      constexpr uint32_t id_s = idesc_f16(false, 128, 128, false, false);
+      constexpr uint32_t id_o = idesc_f16(false, 128, D, false, true);
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
       auto issue_s = [&](int t, int g) {
         const uint64_t a0 = sdesc_add(q_desc, t * L::kTile), b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kQParts; ++q)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            umma_ss_f8(tmem + t * 128, sdesc_add(a0, q * 2 * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
-                       id_s | (q < 2 ? 0u : kE5M2A),
-                       (q > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
+          umma_ss(tmem + t * 128, sdesc_add(a0, o), sdesc_add(b0, o), id_s, kk > 0 ? 1u : 0u);
+        }
         umma_commit(&s_full[t]);
       };
       auto issue_o = [&](int t, int g, bool acc, int half) {
         const uint64_t b0 = sdesc_add(v_desc, (g % kStages) * L::kTile);
 #pragma unroll
-        for (int q = 0; q < kPParts; ++q)
-#pragma unroll
-          for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
-            umma_ts_f8(tmem + 256 + t * 128, tmem + t * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
-                         id_o | (q < 2 ? 0u : kE5M2A),
-                       (acc || q > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+          umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_add(b0, kk * 2048), id_o,
+                  (acc || kk > 0) ? 1u : 0u);
       };
       CacheWalk<kRows> walk;
       walk.start(p, run.first);
@@ -1207,7 +1214,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int it = 0; ok && it < left; ++it, ++g) {
           const int s = g % kStages;
-          if (!mbar_wait(&v_clean[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
           bool next_k = false;
           for (int t = 0; t < nq; ++t) {
             const int u = steps[t]++;
@@ -1234,11 +1241,90 @@ __global__ void __launch_bounds__(384, 1)
       umma_commit(mma_done);
       int drain = 0;
       mbar_wait(mma_done, 0, &drain);
-    } else if (warp == 10) {
-      cache_cleaner<kRows, kStages>(p, run, smem + L::kVOff, v_full, v_clean, abort_flag);
+    }
+  } else if (warp >= 8) {
+    if (run.count > 0) {
+      // ---------------------------------------------------------------- conversion
+      constexpr int kPerRow = D / 16;           // 16-byte pieces (16 codes) per token
+      constexpr int kIt = 128 * kPerRow / 128;  // pieces per thread of K, and of V
+      const int t = threadIdx.x - 256, col = t % kPerRow, row0 = t / kPerRow;
+      constexpr int kStep = 128 / kPerRow;      // tokens between a thread's pieces
+      CacheWalk<kRows> walk;
+      walk.start(p, run.first);
+      // Lane l (and l + 8, ...) looks up key group l: the page number of the tile the walk is at, loaded a tile ahead.
+      const int grp = lane & 7;
+      auto page_of = [&]() {
+        const CacheItem& c = walk.item;
+        const int key = cache_key0(c, walk.at.w) + grp * 16, n = key / p.page, pk = n * p.page;
+        int id = -1;
+        if (n < p.max_pages && pk <= c.key_hi && (pk + p.page > c.key_lo || pk < p.sinks))
+          id = __ldg(p.table + static_cast<size_t>(c.b) * p.max_pages + n);
+        return id;
+      };
+      int id = page_of();
+      uint4 kv[2][kIt];
+      float ks = 0.f, vs = 0.f;
+      bool has = false;
+      auto load = [&]() {  // the tile the walk is at; then on to the next
+        const CacheItem c = walk.item;
+        const int key0 = cache_key0(c, walk.at.w), hk = walk.at.hk;
+        has = id >= 0 && id < p.num_pages;
+        if (has) {
+          const size_t at = static_cast<size_t>(id) * p.Hkv + hk;
+          ks = __ldg(p.k_scale + at);
+          vs = __ldg(p.v_scale + at);
+        }
+        const int known = has ? id : -1;
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int row = row0 + i * kStep, key = key0 + row;
+          const int pid = __shfl_sync(0xffffffffu, known, row / 16);
+          kv[0][i] = kv[1][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (pid >= 0 && key <= c.key_hi && (key >= c.key_lo || key < p.sinks)) {
+            const size_t at = ((static_cast<size_t>(pid) * p.Hkv + hk) * p.page + key % p.page) * D + col * 16;
+            kv[0][i] = __ldg(reinterpret_cast<const uint4*>(p.k_pages + at));
+            kv[1][i] = __ldg(reinterpret_cast<const uint4*>(p.v_pages + at));
+          }
+        }
+      };
+      load();
+      for (int g = 0; g < run.count; ++g) {
+        const int s = g % kStages;
+        if (g + 1 < run.count) {
+          walk.advance(p, 1);
+          id = page_of();
+        }
+        const bool got = g < kStages || mbar_wait(&kv_empty[s], ((g / kStages) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) break;
+        if (t < 8) {
+          fac[s * 24 + t] = has ? ks : 0.f;
+          fac[s * 24 + 8 + t] = has ? log2f(vs) : -INFINITY;  // a key without a page has weight 0
+          fac[s * 24 + 16 + t] = has ? 1.f / vs : 0.f;
+        }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          uint8_t* tile = smem + (which ? L::kVOff : L::kKOff) + s * L::kTile + (col / 4) * 16384;
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) {
+            const int row = row0 + i * kStep, unit = (col % 4) * 2;
+            const uint32_t w[4] = {kv[which][i].x, kv[which][i].y, kv[which][i].z, kv[which][i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[2 * e] = f16x2_from_e4m3x2(w[e] & 0xffffu);
+              h[2 * e + 1] = f16x2_from_e4m3x2(w[e] >> 16);
+            }
+            *reinterpret_cast<uint4*>(tile + row * 128 + ((unit ^ (row & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(tile + row * 128 + (((unit + 1) ^ (row & 7)) * 16)) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(which ? &v_full[s] : &k_full[s]);
+        }
+        if (g + 1 < run.count) load();
+      }
     }
   } else {
-    regs_inc<208>();
     // ------------------------------------------------------------------ softmax warpgroups (thread = row)
     const int t = warp / 4;
     const uint32_t quarter = warp % 4;
@@ -1272,14 +1358,21 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < D / 8; ++i) amax = q_amax8<kBF16>(src[i], amax);
         float mul, back;
         q_row_scale(amax, mul, back);
-        c_row = back * p.scale_log2;
+        c_row = back * fabsf(p.scale_log2);  // the scale's sign goes to q, so that larger scores mean larger weights
+        mul = copysignf(mul, p.scale_log2);
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
-          uint2 part[kQParts];
-          q_split8<kBF16, kQParts, 1>(src[i], mul, part);
-          uint8_t* dst = smem + L::kQOff + t * L::kTile + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
+          const uint4 v = src[i];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t hw[4];
 #pragma unroll
-          for (int q = 0; q < kQParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kTile) = part[q];
+          for (int e = 0; e < 4; ++e) {
+            float a, b;
+            unpack2<kBF16>(w[e], a, b);
+            hw[e] = pack2_f16(a * mul, b * mul);
+          }
+          *reinterpret_cast<uint4*>(smem + L::kQOff + t * L::kTile + (i / 8) * 16384 + r_tile * 128 +
+                                    ((i % 8) ^ (r_tile & 7)) * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_ready[t]);
@@ -1293,34 +1386,37 @@ __global__ void __launch_bounds__(384, 1)
             !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
         if (it > 0 && !mbar_wait(&o_full[t], (step - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
-        float x[128];
-        tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(x));
+        // Two passes over S, 64 columns in registers at a time: the maximum first, then the weights. The exponent of a
+        // weight is s a + log2 vs (a = c ks >= 0 of its 16-key group), so a group's largest is that of its largest s.
         const float* f = fac + s * 24;
         const int key0 = cache_key0(item, w0 + it);
-        // x = s c ks + log2 vs, the weight's exponent
+        const bool masked =
+            key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks);
+        auto hidden = [&](int c) { return key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks); };
+        float m_new = m;
 #pragma unroll
-        for (int gr = 0; gr < 8; ++gr) {
-          const float a = c_row * f[gr], lv = f[8 + gr];
-          const uint64_t a2 = f2_pack(a, a), lv2 = f2_pack(lv, lv);
+        for (int half = 0; half < 2; ++half) {
+          float x[64];
+          tmem_ld_x64(s_tmem + 64 * half, reinterpret_cast<uint32_t*>(x));
+          if (masked) {
 #pragma unroll
-          for (int c = 16 * gr; c < 16 * gr + 16; c += 2) f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), a2, lv2), x[c], x[c + 1]);
+            for (int c = 0; c < 64; ++c)
+              if (hidden(64 * half + c)) x[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) {
+            float g0 = x[16 * gr], g1 = x[16 * gr + 1];
+#pragma unroll
+            for (int c = 2; c < 14; c += 4) {
+              g0 = fmax3(g0, x[16 * gr + c], x[16 * gr + c + 1]);
+              g1 = fmax3(g1, x[16 * gr + c + 2], x[16 * gr + c + 3]);
+            }
+            g0 = fmax3(g0, g1, fmaxf(x[16 * gr + 14], x[16 * gr + 15]));
+            // (a = 0 where there is no page: not 0 * inf)
+            m_new = fmaxf(m_new, g0 == -INFINITY ? g0 : fmaf(g0, c_row * f[4 * half + gr], f[8 + 4 * half + gr]));
+          }
         }
-        if (key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks)) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks)) x[c] = -INFINITY;
-        }
-        float mq[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int c = 4; c < 124; c += 8) {
-          mq[0] = fmax3(mq[0], x[c], x[c + 1]);
-          mq[1] = fmax3(mq[1], x[c + 2], x[c + 3]);
-          mq[2] = fmax3(mq[2], x[c + 4], x[c + 5]);
-          mq[3] = fmax3(mq[3], x[c + 6], x[c + 7]);
-        }
-        const float mx = fmaxf(fmax3(mq[0], mq[1], x[124]), fmax3(mq[2], mq[3], fmax3(x[125], x[126], x[127])));
-        const float m_new = fmaxf(m, mx);
-        if (__any_sync(0xffffffffu, m_new > m + kCacheLag)) {
+        if (__any_sync(0xffffffffu, m_new > m + kManyLag)) {
           const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
           if (it > 0) {
 #pragma unroll
@@ -1336,36 +1432,42 @@ __global__ void __launch_bounds__(384, 1)
           l *= alpha;
           m = m_new;
         }
-        const float off = kCacheShift - (m == -INFINITY ? 0.f : m);
-        const uint64_t off2 = f2_pack(off, off);
+        const float off = kManyShift - (m == -INFINITY ? 0.f : m);
         float lsum = 0.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[kPParts][16];
+          float x[64];
+          uint32_t pk[32];
+          tmem_ld_x64(s_tmem + 64 * half, reinterpret_cast<uint32_t*>(x));
 #pragma unroll
-          for (int gr = 4 * half; gr < 4 * half + 4; ++gr) {
+          for (int gr = 0; gr < 4; ++gr) {
+            const float a = c_row * f[4 * half + gr], b = f[8 + 4 * half + gr] + off;
+            const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
+#pragma unroll
+            for (int c = 16 * gr; c < 16 * gr + 16; c += 2)
+              f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), a2, b2), x[c], x[c + 1]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (hidden(64 * half + c)) x[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) {
             uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
             for (int c = 16 * gr; c < 16 * gr + 16; c += 4) {
-              float w0_, w1_, w2_, w3_;
-              f2_unpack(f2_add(f2_pack(x[c], x[c + 1]), off2), w0_, w1_);
-              f2_unpack(f2_add(f2_pack(x[c + 2], x[c + 3]), off2), w2_, w3_);
-              w0_ = ex2_approx(w0_);
-              w1_ = ex2_approx(w1_);
-              w2_ = ex2_approx(w2_);
-              w3_ = ex2_approx(w3_);
+              const float w0_ = ex2_approx(x[c]), w1_ = ex2_approx(x[c + 1]);
+              const float w2_ = ex2_approx(x[c + 2]), w3_ = ex2_approx(x[c + 3]);
               sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
-              uint32_t part[kPParts];
-              p_split4<kPParts, 1>(w0_, w1_, w2_, w3_, part);
-#pragma unroll
-              for (int q = 0; q < kPParts; ++q) pk[q][(c - 64 * half) / 4] = part[q];
+              pk[c / 2] = pack2_f16(w0_, w1_);
+              pk[c / 2 + 1] = pack2_f16(w2_, w3_);
             }
             float s0, s1;
             f2_unpack(sum2, s0, s1);
-            lsum = fmaf(s0 + s1, f[16 + gr], lsum);
+            lsum = fmaf(s0 + s1, f[16 + 4 * half + gr], lsum);
           }
-#pragma unroll
-          for (int q = 0; q < kPParts; ++q) tmem_st_x16(s_tmem + q * 32 + half * 16, pk[q]);
+          tmem_st_x32(s_tmem + 32 * half, pk);  // (over columns that have been read)
           tmem_st_wait();
           tc_fence_before_sync();
           mbar_arrive(half ? &p_full[t] : &p_half[t]);
@@ -1401,7 +1503,7 @@ __global__ void __launch_bounds__(384, 1)
       if (valid) {
         if (whole)
           p.lse[(static_cast<size_t>(item.b) * p.H + h) * p.Sq + qi] =
-              l == 0.f ? -INFINITY : (m + log2f(l) - kCacheShift) * kLn2;
+              l == 0.f ? -INFINITY : (m + log2f(l) - kManyShift) * kLn2;
         else
           *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m, l);
       }
@@ -1411,7 +1513,7 @@ __global__ void __launch_bounds__(384, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 12) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
   }
