@@ -666,10 +666,10 @@ int launch_cache(const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams
   static bool attr_done[kMaxDevices] = {};
   int rc;
   if constexpr (R == 256) {
-    using L = fa::CacheManySmem<D>;
+    using L = fa::CacheManySmem<D, BF16>;
     auto kern = fa::fa_cache_many_kernel<D, BF16>;
     if ((rc = ensure_smem_attr(kern, L::kAlloc, dev, attr_done))) return rc;
-    kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(p);
+    kern<<<fa::kCacheCtas, L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
   } else {
     using L = fa::CacheSmem<D, BF16, R>;
     auto kern = fa::fa_cache_few_kernel<D, BF16, R>;
@@ -678,7 +678,7 @@ int launch_cache(const CUtensorMap& tk, const CUtensorMap& tv, const CacheParams
   }
   rc = cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   if (rc || !join) return rc;
-  fa::fa_cache_join_kernel<D, BF16, R><<<fa::kCacheCtas, 256, 0, stream>>>(p);
+  fa::fa_cache_join_kernel<D, BF16, R><<<dim3(fa::kCacheCtas, R / 8), 2 * D, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 template <int D, bool BF16>
@@ -770,8 +770,6 @@ int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const 
   p.q = q;
   p.out = out;
   p.lse = lse;
-  p.k_pages = static_cast<const uint8_t*>(k_pages);
-  p.v_pages = static_cast<const uint8_t*>(v_pages);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.table = table;

@@ -44,8 +44,6 @@ struct CacheParams {
   const void* q;         // [B, Sq, H, D]
   void* out;             // [B, Sq, H, D]
   float* lse;            // [B, H, Sq]
-  const uint8_t* k_pages;  // [num_pages, Hkv, page, D] (read through tensor maps for few rows)
-  const uint8_t* v_pages;
   const float* k_scale;  // [num_pages, Hkv]
   const float* v_scale;
   const int* table;      // [B, max_pages]
@@ -368,15 +366,15 @@ __device__ __forceinline__ CacheRun cache_run(const CacheParams& p, CacheScan* s
 // Where a piece of a unit leaves its sums: slot 0 of its CTA if the unit began before, slot 1 if it goes on after.
 __device__ __forceinline__ int cache_slot(int cta, int w0) { return cta * 2 + (w0 > 0 ? 0 : 1); }
 
-// Joins the pieces of every cut unit: CTA c takes the unit whose second piece begins CTA c's run.
+// Joins the pieces of every cut unit: CTA (c, y) takes rows 8 y .. 8 y + 7 of the unit whose second piece begins run c.
 template <int D, bool kBF16, int kRows>
-__global__ void __launch_bounds__(256) fa_cache_join_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(2 * D) fa_cache_join_kernel(const CacheParams p) {
   const int4 cut = p.cuts[blockIdx.x];
   if (cut.x < 0) return;
   const CacheItem t = cache_item<kRows>(p, cut.x);
   const int c_first = blockIdx.x - 1, c_last = cut.z;
-  for (int e = threadIdx.x; e < t.rows * (D / 4); e += blockDim.x) {
-    const int r = e / (D / 4), d = e % (D / 4) * 4;
+  const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  if (r < t.rows) {
     float m = -INFINITY;
     for (int c = c_first; c <= c_last; ++c) {
       const size_t s = static_cast<size_t>(cache_slot(c, c > c_first)) * kRows + r;
@@ -444,11 +442,12 @@ struct CacheSmem {
 // after next and the scales of the next batch are loaded while this batch's copies are issued, so that neither of the two
 // dependent loads is waited for. Pages that no row sees, and page numbers outside the cache, are copied from beyond the
 // tensor's end: the copy engine writes zeros and reads nothing.
-template <int kRows, int kStages>
+// The factors of a tile's key groups go into a ring of kFac places; kFac = kStages: they are published with K.
+template <int kRows, int kStages, int kFac>
 __device__ __forceinline__ void cache_producer(const CacheParams& p, const CacheRun& run, const CUtensorMap& tm_k,
                                                const CUtensorMap& tm_v, uint8_t* smem_k, uint8_t* smem_v, float* fac,
                                                uint64_t* k_full, uint64_t* v_full, uint64_t* kv_empty,
-                                               volatile int* abort_flag) {
+                                               uint64_t* fac_full, volatile int* abort_flag) {
   const int lane = lane_id(), tt = lane >> 3, grp = lane & 7;
   struct Slot {
     int row;  // first row of the page in the [num_pages * Hkv * page, D] view, < 0: none
@@ -514,12 +513,14 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
       __syncwarp();
       if (tt == u) {
         const bool valid = cur.row >= 0;
-        fac[s * 24 + grp] = valid ? cur.ks : 0.f;
-        fac[s * 24 + 8 + grp] = valid ? log2f(cur.vs) : -INFINITY;  // a key without a page has weight 0
-        fac[s * 24 + 16 + grp] = valid ? 1.f / cur.vs : 0.f;
+        float* f = fac + (g % kFac) * 24 + grp;
+        f[0] = valid ? cur.ks : 1.f;
+        f[8] = valid ? log2f(cur.vs) : -INFINITY;  // a key without a page has weight 0
+        f[16] = valid ? 1.f / cur.vs : 0.f;
       }
       __syncwarp();
       if (lane == 0) {
+        if (kFac != kStages) mbar_arrive(&fac_full[g % kFac]);
         mbar_arrive_expect_tx(&k_full[s], 16384);
         mbar_arrive_expect_tx(&v_full[s], 16384);
       }
@@ -726,8 +727,8 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      cache_producer<R, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full, kv_empty,
-                                 abort_flag);
+      cache_producer<R, kStages, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
+                                          kv_empty, nullptr, abort_flag);
     } else if (warp == 9 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
@@ -1101,47 +1102,58 @@ __global__ void __launch_bounds__(384, 1)
 // ------------------------------------------------------------------------------- attention of many query rows
 // Chunks of prompts: units of 256 rows (two 128-row Q tiles, each with its own softmax warpgroup, thread = row), as in
 // the forward of fa_fwd.cuh: while one warpgroup runs the softmax of its tile the tensor core works on the other. With
-// this many rows a key is used often enough that converting it once is cheaper than splitting every weight into 8-bit
-// parts: a converting warpgroup reads the pages (prefetched in registers), and writes K and V as fp16 (exact) into the
-// shared-memory tiles of the 16-bit products; q enters as fp16 scaled per row (exact, as above), the weights in one
-// fp16 rounding. (Splitting measured 788 us where this takes TODO: 4096 tokens of a prompt of 8192, 32 heads on 8, bf16;
-// its conversions to e4m3 run at a quarter of the rate of other arithmetic.) Rows that no query sees are written as 0.
+// this many rows splitting every weight into 8-bit parts would cost more than converting V once: two converting warps
+// turn each arrived tile of V into an fp16 tile (exact), the weights are fp16 in one rounding, and PV is a 16-bit
+// product. K stays e4m3: q's parts are made once per unit, and the parts' products take as long as one 16-bit product
+// (bf16). (Weights in parts: 788 us for 4096 tokens of a prompt of 8192, 32 heads on 8, bf16; K and V converted: 644 to
+// 738 us; this: TODO us.) V rows that no query sees are written as 0.
 //
-// Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8-11 conversion, 12 MMA, 13-15 idle. TMEM columns: S0 [0,128),
-// S1 [128,256), O0 [256,256+D), O1 [384,384+D); P_t overwrites the first 64 columns of S_t.
-template <int D>
+// Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8 TMA, 9 MMA, 10-11 conversion. TMEM columns: S0 [0,128), S1 [128,256),
+// O0 [256,256+D), O1 [384,384+D); P_t overwrites the first 64 columns of S_t.
+template <int D, bool kBF16>
 struct CacheManySmem {
-  static constexpr int kRows = 256, kStages = 2;
-  static constexpr int kTile = 128 * D * 2;           // 128 rows of fp16: D / 64 chunks of 128-byte swizzle rows
-  static constexpr int kQOff = 0;                     // [Q tile]
-  static constexpr int kKOff = kQOff + 2 * kTile;
-  static constexpr int kVOff = kKOff + kStages * kTile;
-  static constexpr int kFacOff = kVOff + kStages * kTile;
-  static constexpr int kBarOff = kFacOff + kStages * 96;
-  static constexpr int kNumBars = 3 * kStages + 11;
+  static constexpr int kRows = 256, kStages = 3, kFac = 4;
+  static constexpr int kQParts = kBF16 ? 2 : 3;
+  static constexpr int kRaw = 16384;                  // 128 rows of e4m3, 128-byte swizzle rows (a part of q, K or V)
+  static constexpr int kTile = 128 * D * 2;           // fp16 V: D / 64 chunks of 128-byte swizzle rows
+  static constexpr int kVBuf = kBF16 || D == 64 ? 2 : 1;  // fp16 V tiles (what fits beside three parts of q)
+  static constexpr int kQOff = 0;                     // [part][Q tile]
+  static constexpr int kVOff = kQOff + kQParts * 2 * kRaw;
+  static constexpr int kKRawOff = kVOff + kVBuf * kTile;  // [kStages]
+  static constexpr int kVRawOff = kKRawOff + kStages * kRaw;
+  static constexpr int kFacOff = kVRawOff + kStages * kRaw;
+  static constexpr int kBarOff = kFacOff + kFac * 96;
+  static constexpr int kNumBars = 3 * kStages + 2 * kVBuf + kFac + 11;
   static constexpr int kScanOff = kBarOff + kNumBars * 8;
   static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 384;
+  static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;  // 2 * 128 * 208 + 128 * 88 = 384 * 168
   static constexpr uint32_t kTmemCols = 512;
+  static constexpr bool kSplitP = D == 64;  // P handed over in two halves (as in fa_fwd.cuh)
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams p) {
-  using L = CacheManySmem<D>;
-  constexpr int kStages = L::kStages, kRows = L::kRows;
+__global__ void __launch_bounds__(384, 1)
+    fa_cache_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const CacheParams p) {
+  using L = CacheManySmem<D, kBF16>;
+  constexpr int kStages = L::kStages, kRows = L::kRows, kQParts = L::kQParts, kVBuf = L::kVBuf;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint64_t* k_full = bars;                // [kStages]
-  uint64_t* v_full = k_full + kStages;    // [kStages]
-  uint64_t* kv_empty = v_full + kStages;  // [kStages]
-  uint64_t* s_full = kv_empty + kStages;  // [2]
-  uint64_t* p_half = s_full + 2;          // [2] weights of keys 0..63 published
-  uint64_t* p_full = s_full + 4;          // [2]
-  uint64_t* o_full = s_full + 6;          // [2]
-  uint64_t* q_ready = s_full + 8;         // [2]
+  uint64_t* k_raw = bars;                  // [kStages] K and V tiles arrived
+  uint64_t* v_raw = k_raw + kStages;       // [kStages]
+  uint64_t* raw_empty = v_raw + kStages;   // [kStages] K's products done, V converted
+  uint64_t* v_full = raw_empty + kStages;  // [kVBuf] fp16 V written
+  uint64_t* v_empty = v_full + kVBuf;      // [kVBuf] its products done
+  uint64_t* fac_full = v_empty + kVBuf;    // [kFac]
+  uint64_t* s_full = fac_full + L::kFac;   // [2]
+  uint64_t* p_half = s_full + 2;           // [2] weights of keys 0..63 published (kSplitP)
+  uint64_t* p_full = s_full + 4;           // [2]
+  uint64_t* o_full = s_full + 6;           // [2]
+  uint64_t* q_ready = s_full + 8;          // [2]
   uint64_t* mma_done = s_full + 10;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
@@ -1150,9 +1162,9 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], 128);
-      mbar_init(&v_full[s], 128);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_raw[s], 1);
+      mbar_init(&v_raw[s], 1);
+      mbar_init(&raw_empty[s], 65);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -1161,11 +1173,16 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
       mbar_init(&o_full[t], 1);
       mbar_init(&q_ready[t], 128);
     }
+    for (int s = 0; s < kVBuf; ++s) {
+      mbar_init(&v_full[s], 64);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < L::kFac; ++s) mbar_init(&fac_full[s], 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 9) {
     tmem_alloc(tmem_holder, L::kTmemCols);
     tmem_relinquish();
   }
@@ -1174,25 +1191,36 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
   const CacheRun run = cache_run<kRows, L::kThreads>(p, reinterpret_cast<CacheScan*>(smem + L::kScanOff));
-  if (warp >= 12) {
-    if (warp == 12 && lane == 0 && run.count > 0) {
+  if (warp >= 8) {
+    regs_dec<L::kRegsOther>();
+    if (run.count == 0) {
+    } else if (warp == 8) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      cache_producer<kRows, kStages, L::kFac>(p, run, tm_k, tm_v, smem + L::kKRawOff, smem + L::kVRawOff, fac, k_raw,
+                                              v_raw, raw_empty, fac_full, abort_flag);
+    } else if (warp == 9 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_f16(false, 128, 128, false, false);
+      constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);
       constexpr uint32_t id_o = idesc_f16(false, 128, D, false, true);
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKRawOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
-      auto issue_s = [&](int t, int g) {
-        const uint64_t a0 = sdesc_add(q_desc, t * L::kTile), b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
+      auto issue_s = [&](int t, int g, bool last) {
+        const uint64_t a0 = sdesc_add(q_desc, t * L::kRaw), b0 = sdesc_add(k_desc, (g % kStages) * L::kRaw);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
-          umma_ss(tmem + t * 128, sdesc_add(a0, o), sdesc_add(b0, o), id_s, kk > 0 ? 1u : 0u);
-        }
+        for (int q = 0; q < kQParts; ++q)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_ss_f8(tmem + t * 128, sdesc_add(a0, q * 2 * L::kRaw + kk * 32), sdesc_add(b0, kk * 32),
+                       id_s | (part_is_e5m2(q, 1) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&s_full[t]);
+        if (last) umma_commit(&raw_empty[g % kStages]);
       };
       auto issue_o = [&](int t, int g, bool acc, int half) {
-        const uint64_t b0 = sdesc_add(v_desc, (g % kStages) * L::kTile);
+        const uint64_t b0 = sdesc_add(v_desc, (g % kVBuf) * L::kTile);
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
           umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_add(b0, kk * 2048), id_o,
@@ -1205,126 +1233,94 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
       for (int g = 0; ok && g < run.count;) {
         const int left = min(run.count - g, walk.item.n - walk.at.w);  // tiles of this unit in the run
         const int nq = walk.item.rows > 128 ? 2 : 1;                   // Q tiles with rows
-        ok = mbar_wait(&k_full[g % kStages], (g / kStages) & 1, abort_flag);
+        ok = mbar_wait(&k_raw[g % kStages], (g / kStages) & 1, abort_flag);
         for (int t = 0; ok && t < nq; ++t) {
           ok = mbar_wait(&q_ready[t], units[t]++ & 1, abort_flag);
           if (!ok) break;
           tc_fence_after_sync();
-          issue_s(t, g);
+          issue_s(t, g, t == nq - 1);
         }
         for (int it = 0; ok && it < left; ++it, ++g) {
-          const int s = g % kStages;
-          if (!mbar_wait(&v_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&v_full[g % kVBuf], (g / kVBuf) & 1, abort_flag)) { ok = false; break; }
           bool next_k = false;
           for (int t = 0; t < nq; ++t) {
             const int u = steps[t]++;
-            if (!mbar_wait(&p_half[t], u & 1, abort_flag)) { ok = false; break; }
+            if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
             issue_o(t, g, it > 0, 0);
-            if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after_sync();
+            if (L::kSplitP) {
+              if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
+              tc_fence_after_sync();
+            }
             issue_o(t, g, true, 1);
             umma_commit(&o_full[t]);
+            if (t == nq - 1) umma_commit(&v_empty[g % kVBuf]);
             if (it + 1 < left) {
               if (!next_k) {
-                if (!mbar_wait(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
+                if (!mbar_wait(&k_raw[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after_sync();
                 next_k = true;
               }
-              issue_s(t, g + 1);
+              issue_s(t, g + 1, t == nq - 1);
             }
           }
-          umma_commit(&kv_empty[s]);
         }
         if (ok && g < run.count) walk.advance(p, left);
       }
       umma_commit(mma_done);
       int drain = 0;
       mbar_wait(mma_done, 0, &drain);
-    }
-  } else if (warp >= 8) {
-    if (run.count > 0) {
+    } else if (warp >= 10) {
       // ---------------------------------------------------------------- conversion
-      constexpr int kPerRow = D / 16;           // 16-byte pieces (16 codes) per token
-      constexpr int kIt = 128 * kPerRow / 128;  // pieces per thread of K, and of V
-      const int t = threadIdx.x - 256, col = t % kPerRow, row0 = t / kPerRow;
-      constexpr int kStep = 128 / kPerRow;      // tokens between a thread's pieces
+      // A thread takes 16-byte pieces (16 codes) of one column of the tile; eight neighbouring threads take eight rows, so
+      // that neither the reads nor the writes of the swizzled rows meet in a bank.
+      constexpr int kPerRow = D / 16;
+      const int t = threadIdx.x - 320, col = (t >> 3) % kPerRow, row0 = (t & 7) + 8 * ((t >> 3) / kPerRow);
+      constexpr int kStep = 64 / kPerRow;  // tokens between a thread's pieces
       CacheWalk<kRows> walk;
       walk.start(p, run.first);
-      // Lane l (and l + 8, ...) looks up key group l: the page number of the tile the walk is at, loaded a tile ahead.
-      const int grp = lane & 7;
-      auto page_of = [&]() {
-        const CacheItem& c = walk.item;
-        const int key = cache_key0(c, walk.at.w) + grp * 16, n = key / p.page, pk = n * p.page;
-        int id = -1;
-        if (n < p.max_pages && pk <= c.key_hi && (pk + p.page > c.key_lo || pk < p.sinks))
-          id = __ldg(p.table + static_cast<size_t>(c.b) * p.max_pages + n);
-        return id;
-      };
-      int id = page_of();
-      uint4 kv[2][kIt];
-      float ks = 0.f, vs = 0.f;
-      bool has = false;
-      auto load = [&]() {  // the tile the walk is at; then on to the next
-        const CacheItem c = walk.item;
-        const int key0 = cache_key0(c, walk.at.w), hk = walk.at.hk;
-        has = id >= 0 && id < p.num_pages;
-        if (has) {
-          const size_t at = static_cast<size_t>(id) * p.Hkv + hk;
-          ks = __ldg(p.k_scale + at);
-          vs = __ldg(p.v_scale + at);
-        }
-        const int known = has ? id : -1;
+      auto convert = [&](const uint8_t* raw, uint8_t* tile, auto keep) {
+        const int x = t & 7, unit = (col % 4) * 2;  // (row & 7 is the same for all of a thread's rows)
+        raw += row0 * 128 + ((col ^ x) * 16);
+        uint8_t* dst0 = tile + (col / 4) * 16384 + row0 * 128 + ((unit ^ x) * 16);
+        uint8_t* dst1 = tile + (col / 4) * 16384 + row0 * 128 + (((unit + 1) ^ x) * 16);
+#pragma unroll 8
+        for (int i = 0; i < 128 / kStep; ++i) {
+          uint4 v = *reinterpret_cast<const uint4*>(raw + i * kStep * 128);
+          if (!keep(row0 + i * kStep)) v = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const int row = row0 + i * kStep, key = key0 + row;
-          const int pid = __shfl_sync(0xffffffffu, known, row / 16);
-          kv[0][i] = kv[1][i] = make_uint4(0u, 0u, 0u, 0u);
-          if (pid >= 0 && key <= c.key_hi && (key >= c.key_lo || key < p.sinks)) {
-            const size_t at = ((static_cast<size_t>(pid) * p.Hkv + hk) * p.page + key % p.page) * D + col * 16;
-            kv[0][i] = __ldg(reinterpret_cast<const uint4*>(p.k_pages + at));
-            kv[1][i] = __ldg(reinterpret_cast<const uint4*>(p.v_pages + at));
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = f16x2_from_e4m3x2(w[e] & 0xffffu);
+            h[2 * e + 1] = f16x2_from_e4m3x2(w[e] >> 16);
           }
+          *reinterpret_cast<uint4*>(dst0 + i * kStep * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst1 + i * kStep * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
+        fence_proxy_async_smem();
       };
-      load();
       for (int g = 0; g < run.count; ++g) {
-        const int s = g % kStages;
-        if (g + 1 < run.count) {
-          walk.advance(p, 1);
-          id = page_of();
-        }
-        const bool got = g < kStages || mbar_wait(&kv_empty[s], ((g / kStages) - 1) & 1, abort_flag);
+        const int s = g % kStages, b = g % kVBuf;
+        const CacheItem& c = walk.item;
+        const int key0 = cache_key0(c, walk.at.w);
+        const bool got = mbar_wait(&v_raw[s], (g / kStages) & 1, abort_flag) &&
+                         (g < kVBuf || mbar_wait(&v_empty[b], ((g / kVBuf) - 1) & 1, abort_flag));
         if (!__all_sync(0xffffffffu, got)) break;
-        if (t < 8) {
-          fac[s * 24 + t] = has ? ks : 0.f;
-          fac[s * 24 + 8 + t] = has ? log2f(vs) : -INFINITY;  // a key without a page has weight 0
-          fac[s * 24 + 16 + t] = has ? 1.f / vs : 0.f;
-        }
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          uint8_t* tile = smem + (which ? L::kVOff : L::kKOff) + s * L::kTile + (col / 4) * 16384;
-#pragma unroll
-          for (int i = 0; i < kIt; ++i) {
-            const int row = row0 + i * kStep, unit = (col % 4) * 2;
-            const uint32_t w[4] = {kv[which][i].x, kv[which][i].y, kv[which][i].z, kv[which][i].w};
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = f16x2_from_e4m3x2(w[e] & 0xffffu);
-              h[2 * e + 1] = f16x2_from_e4m3x2(w[e] >> 16);
-            }
-            *reinterpret_cast<uint4*>(tile + row * 128 + ((unit ^ (row & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(tile + row * 128 + (((unit + 1) ^ (row & 7)) * 16)) =
-                make_uint4(h[4], h[5], h[6], h[7]);
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(which ? &v_full[s] : &k_full[s]);
-        }
-        if (g + 1 < run.count) load();
+        // Rows that no query sees are 0: their weights are, but a stale byte may be a NaN.
+        if (cache_ragged(p, c, key0))
+          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff + b * L::kTile, [&](int row) {
+            return key0 + row <= c.key_hi && (key0 + row >= c.key_lo || key0 + row < p.sinks);
+          });
+        else
+          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff + b * L::kTile, [](int) { return true; });
+        mbar_arrive(&v_full[b]);
+        mbar_arrive(&raw_empty[s]);
+        if (g + 1 < run.count) walk.advance(p, 1);
       }
     }
   } else {
+    regs_inc<L::kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax warpgroups (thread = row)
     const int t = warp / 4;
     const uint32_t quarter = warp % 4;
@@ -1359,20 +1355,15 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
         float mul, back;
         q_row_scale(amax, mul, back);
         c_row = back * fabsf(p.scale_log2);  // the scale's sign goes to q, so that larger scores mean larger weights
+        c_row = c_row < 1e-37f ? 1e-37f : c_row;  // (never 0: a masked score is -inf)
         mul = copysignf(mul, p.scale_log2);
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = src[i];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t hw[4];
+          uint2 part[kQParts];
+          q_split8<kBF16, kQParts, 1>(src[i], mul, part);
+          uint8_t* dst = smem + L::kQOff + t * L::kRaw + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a, b;
-            unpack2<kBF16>(w[e], a, b);
-            hw[e] = pack2_f16(a * mul, b * mul);
-          }
-          *reinterpret_cast<uint4*>(smem + L::kQOff + t * L::kTile + (i / 8) * 16384 + r_tile * 128 +
-                                    ((i % 8) ^ (r_tile & 7)) * 16) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          for (int q = 0; q < kQParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kRaw) = part[q];
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_ready[t]);
@@ -1381,40 +1372,32 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
       const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
       float m = -INFINITY, l = 0.f;
       for (int it = 0; it < left; ++it, ++g, ++step) {
-        const int s = g % kStages;
         if (!mbar_wait(&s_full[t], step & 1, abort_flag) ||
-            !mbar_wait(&k_full[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
+            !mbar_wait(&fac_full[g % L::kFac], (g / L::kFac) & 1, abort_flag)) { ok = false; break; }
         if (it > 0 && !mbar_wait(&o_full[t], (step - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after_sync();
-        // Two passes over S, 64 columns in registers at a time: the maximum first, then the weights. The exponent of a
-        // weight is s a + log2 vs (a = c ks >= 0 of its 16-key group), so a group's largest is that of its largest s.
-        const float* f = fac + s * 24;
+        float x[128];
+        tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(x));
+        const float* f = fac + (g % L::kFac) * 24;
         const int key0 = cache_key0(item, w0 + it);
-        const bool masked =
-            key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks);
-        auto hidden = [&](int c) { return key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks); };
+        if (key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (key0 + c > aligned || (key0 + c < from && key0 + c >= p.sinks)) x[c] = -INFINITY;
+        }
+        // The exponent of a weight is s a + log2 vs (a = c ks > 0 of its 16-key group), so a group's largest is that of
+        // its largest s.
         float m_new = m;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[64];
-          tmem_ld_x64(s_tmem + 64 * half, reinterpret_cast<uint32_t*>(x));
-          if (masked) {
+        for (int gr = 0; gr < 8; ++gr) {
+          float g0 = x[16 * gr], g1 = x[16 * gr + 1];
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (hidden(64 * half + c)) x[c] = -INFINITY;
+          for (int c = 2; c < 14; c += 4) {
+            g0 = fmax3(g0, x[16 * gr + c], x[16 * gr + c + 1]);
+            g1 = fmax3(g1, x[16 * gr + c + 2], x[16 * gr + c + 3]);
           }
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            float g0 = x[16 * gr], g1 = x[16 * gr + 1];
-#pragma unroll
-            for (int c = 2; c < 14; c += 4) {
-              g0 = fmax3(g0, x[16 * gr + c], x[16 * gr + c + 1]);
-              g1 = fmax3(g1, x[16 * gr + c + 2], x[16 * gr + c + 3]);
-            }
-            g0 = fmax3(g0, g1, fmaxf(x[16 * gr + 14], x[16 * gr + 15]));
-            // (a = 0 where there is no page: not 0 * inf)
-            m_new = fmaxf(m_new, g0 == -INFINITY ? g0 : fmaf(g0, c_row * f[4 * half + gr], f[8 + 4 * half + gr]));
-          }
+          g0 = fmax3(g0, g1, fmaxf(x[16 * gr + 14], x[16 * gr + 15]));
+          m_new = fmaxf(m_new, fmaf(g0, c_row * f[gr], f[8 + gr]));
         }
         if (__any_sync(0xffffffffu, m_new > m + kManyLag)) {
           const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
@@ -1434,44 +1417,42 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
         }
         const float off = kManyShift - (m == -INFINITY ? 0.f : m);
         float lsum = 0.f;
+        uint32_t pk[64];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[64];
-          uint32_t pk[32];
-          tmem_ld_x64(s_tmem + 64 * half, reinterpret_cast<uint32_t*>(x));
+        for (int gr = 0; gr < 8; ++gr) {
+          const float a = c_row * f[gr], b = f[8 + gr] + off;
+          const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
+          uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            const float a = c_row * f[4 * half + gr], b = f[8 + 4 * half + gr] + off;
-            const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
-#pragma unroll
-            for (int c = 16 * gr; c < 16 * gr + 16; c += 2)
-              f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), a2, b2), x[c], x[c + 1]);
+          for (int c = 16 * gr; c < 16 * gr + 16; c += 4) {
+            float w0_, w1_, w2_, w3_;
+            f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), a2, b2), w0_, w1_);
+            f2_unpack(f2_fma(f2_pack(x[c + 2], x[c + 3]), a2, b2), w2_, w3_);
+            w0_ = ex2_approx(w0_);
+            w1_ = ex2_approx(w1_);
+            w2_ = ex2_approx(w2_);
+            w3_ = ex2_approx(w3_);
+            sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
+            pk[c / 2] = pack2_f16(w0_, w1_);
+            pk[c / 2 + 1] = pack2_f16(w2_, w3_);
           }
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (hidden(64 * half + c)) x[c] = -INFINITY;
+          float s0, s1;
+          f2_unpack(sum2, s0, s1);
+          lsum = fmaf(s0 + s1, f[16 + gr], lsum);
+          if (L::kSplitP && gr == 3) {
+            tmem_st_x32(s_tmem, pk);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            mbar_arrive(&p_half[t]);
           }
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            uint64_t sum2 = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int c = 16 * gr; c < 16 * gr + 16; c += 4) {
-              const float w0_ = ex2_approx(x[c]), w1_ = ex2_approx(x[c + 1]);
-              const float w2_ = ex2_approx(x[c + 2]), w3_ = ex2_approx(x[c + 3]);
-              sum2 = f2_add(sum2, f2_add(f2_pack(w0_, w1_), f2_pack(w2_, w3_)));
-              pk[c / 2] = pack2_f16(w0_, w1_);
-              pk[c / 2 + 1] = pack2_f16(w2_, w3_);
-            }
-            float s0, s1;
-            f2_unpack(sum2, s0, s1);
-            lsum = fmaf(s0 + s1, f[16 + 4 * half + gr], lsum);
-          }
-          tmem_st_x32(s_tmem + 32 * half, pk);  // (over columns that have been read)
-          tmem_st_wait();
-          tc_fence_before_sync();
-          mbar_arrive(half ? &p_full[t] : &p_half[t]);
         }
+        if (L::kSplitP)
+          tmem_st_x32(s_tmem + 32, pk + 32);
+        else
+          tmem_st_x64(s_tmem, pk);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&p_full[t]);
         l += lsum;
       }
       if (!ok) break;
@@ -1513,7 +1494,7 @@ __global__ void __launch_bounds__(512, 1) fa_cache_many_kernel(const CacheParams
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 9) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
   }
