@@ -1106,24 +1106,23 @@ __global__ void __launch_bounds__(384, 1)
 // turn each arrived tile of V into an fp16 tile (exact), the weights are fp16 in one rounding, and PV is a 16-bit
 // product. K stays e4m3: q's parts are made once per unit, and the parts' products take as long as one 16-bit product
 // (bf16). (Weights in parts: 788 us for 4096 tokens of a prompt of 8192, 32 heads on 8, bf16; K and V converted: 644 to
-// 738 us; this: TODO us.) V rows that no query sees are written as 0.
+// 738 us; this: 511 us, where the forward on 16-bit K and V of that length takes 399 us.) V rows that no query sees are written as 0.
 //
 // Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8 TMA, 9 MMA, 10-11 conversion. TMEM columns: S0 [0,128), S1 [128,256),
 // O0 [256,256+D), O1 [384,384+D); P_t overwrites the first 64 columns of S_t.
 template <int D, bool kBF16>
 struct CacheManySmem {
-  static constexpr int kRows = 256, kStages = 3, kFac = 4;
+  static constexpr int kRows = 256, kStages = 2, kFac = 4;
   static constexpr int kQParts = kBF16 ? 2 : 3;
   static constexpr int kRaw = 16384;                  // 128 rows of e4m3, 128-byte swizzle rows (a part of q, K or V)
   static constexpr int kTile = 128 * D * 2;           // fp16 V: D / 64 chunks of 128-byte swizzle rows
-  static constexpr int kVBuf = kBF16 || D == 64 ? 2 : 1;  // fp16 V tiles (what fits beside three parts of q)
   static constexpr int kQOff = 0;                     // [part][Q tile]
   static constexpr int kVOff = kQOff + kQParts * 2 * kRaw;
-  static constexpr int kKRawOff = kVOff + kVBuf * kTile;  // [kStages]
+  static constexpr int kKRawOff = kVOff + kTile;      // [kStages]
   static constexpr int kVRawOff = kKRawOff + kStages * kRaw;
   static constexpr int kFacOff = kVRawOff + kStages * kRaw;
   static constexpr int kBarOff = kFacOff + kFac * 96;
-  static constexpr int kNumBars = 3 * kStages + 2 * kVBuf + kFac + 11;
+  static constexpr int kNumBars = 3 * kStages + 2 + kFac + 11;
   static constexpr int kScanOff = kBarOff + kNumBars * 8;
   static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
   static constexpr int kAlloc = kMiscOff + 16 + 1024;
@@ -1139,16 +1138,16 @@ __global__ void __launch_bounds__(384, 1)
     fa_cache_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const CacheParams p) {
   using L = CacheManySmem<D, kBF16>;
-  constexpr int kStages = L::kStages, kRows = L::kRows, kQParts = L::kQParts, kVBuf = L::kVBuf;
+  constexpr int kStages = L::kStages, kRows = L::kRows, kQParts = L::kQParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* k_raw = bars;                  // [kStages] K and V tiles arrived
   uint64_t* v_raw = k_raw + kStages;       // [kStages]
   uint64_t* raw_empty = v_raw + kStages;   // [kStages] K's products done, V converted
-  uint64_t* v_full = raw_empty + kStages;  // [kVBuf] fp16 V written
-  uint64_t* v_empty = v_full + kVBuf;      // [kVBuf] its products done
-  uint64_t* fac_full = v_empty + kVBuf;    // [kFac]
+  uint64_t* v_full = raw_empty + kStages;  // fp16 V written
+  uint64_t* v_empty = v_full + 1;          // its products done
+  uint64_t* fac_full = v_empty + 1;        // [kFac]
   uint64_t* s_full = fac_full + L::kFac;   // [2]
   uint64_t* p_half = s_full + 2;           // [2] weights of keys 0..63 published (kSplitP)
   uint64_t* p_full = s_full + 4;           // [2]
@@ -1173,10 +1172,8 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&o_full[t], 1);
       mbar_init(&q_ready[t], 128);
     }
-    for (int s = 0; s < kVBuf; ++s) {
-      mbar_init(&v_full[s], 64);
-      mbar_init(&v_empty[s], 1);
-    }
+    mbar_init(v_full, 64);
+    mbar_init(v_empty, 1);
     for (int s = 0; s < L::kFac; ++s) mbar_init(&fac_full[s], 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -1219,11 +1216,10 @@ __global__ void __launch_bounds__(384, 1)
         umma_commit(&s_full[t]);
         if (last) umma_commit(&raw_empty[g % kStages]);
       };
-      auto issue_o = [&](int t, int g, bool acc, int half) {
-        const uint64_t b0 = sdesc_add(v_desc, (g % kVBuf) * L::kTile);
+      auto issue_o = [&](int t, bool acc, int half) {
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-          umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_add(b0, kk * 2048), id_o,
+          umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, sdesc_add(v_desc, kk * 2048), id_o,
                   (acc || kk > 0) ? 1u : 0u);
       };
       CacheWalk<kRows> walk;
@@ -1241,20 +1237,20 @@ __global__ void __launch_bounds__(384, 1)
           issue_s(t, g, t == nq - 1);
         }
         for (int it = 0; ok && it < left; ++it, ++g) {
-          if (!mbar_wait(&v_full[g % kVBuf], (g / kVBuf) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(v_full, g & 1, abort_flag)) { ok = false; break; }
           bool next_k = false;
           for (int t = 0; t < nq; ++t) {
             const int u = steps[t]++;
             if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
-            issue_o(t, g, it > 0, 0);
+            issue_o(t, it > 0, 0);
             if (L::kSplitP) {
               if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
               tc_fence_after_sync();
             }
-            issue_o(t, g, true, 1);
+            issue_o(t, true, 1);
             umma_commit(&o_full[t]);
-            if (t == nq - 1) umma_commit(&v_empty[g % kVBuf]);
+            if (t == nq - 1) umma_commit(v_empty);
             if (it + 1 < left) {
               if (!next_k) {
                 if (!mbar_wait(&k_raw[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
@@ -1301,20 +1297,20 @@ __global__ void __launch_bounds__(384, 1)
         fence_proxy_async_smem();
       };
       for (int g = 0; g < run.count; ++g) {
-        const int s = g % kStages, b = g % kVBuf;
+        const int s = g % kStages;
         const CacheItem& c = walk.item;
         const int key0 = cache_key0(c, walk.at.w);
         const bool got = mbar_wait(&v_raw[s], (g / kStages) & 1, abort_flag) &&
-                         (g < kVBuf || mbar_wait(&v_empty[b], ((g / kVBuf) - 1) & 1, abort_flag));
+                         (g == 0 || mbar_wait(v_empty, (g - 1) & 1, abort_flag));
         if (!__all_sync(0xffffffffu, got)) break;
         // Rows that no query sees are 0: their weights are, but a stale byte may be a NaN.
         if (cache_ragged(p, c, key0))
-          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff + b * L::kTile, [&](int row) {
+          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff, [&](int row) {
             return key0 + row <= c.key_hi && (key0 + row >= c.key_lo || key0 + row < p.sinks);
           });
         else
-          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff + b * L::kTile, [](int) { return true; });
-        mbar_arrive(&v_full[b]);
+          convert(smem + L::kVRawOff + s * L::kRaw, smem + L::kVOff, [](int) { return true; });
+        mbar_arrive(v_full);
         mbar_arrive(&raw_empty[s]);
         if (g + 1 < run.count) walk.advance(p, 1);
       }
@@ -1332,7 +1328,7 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     int step = 0;  // tiles this Q tile has taken part in
     for (int g = 0; ok && g < run.count;) {
-      const CacheItem item = walk.item;
+      const CacheItem& item = walk.item;
       const int hk = walk.at.hk, w0 = walk.at.w;
       const int left = min(run.count - g, item.n - w0);
       if (item.rows <= t * 128) {  // no rows in this Q tile
@@ -1378,7 +1374,7 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after_sync();
         float x[128];
         tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(x));
-        const float* f = fac + (g % L::kFac) * 24;
+        const float* f = fac + (g % L::kFac) * 24;  // ks, log2 vs, 1 / vs of the tile's eight key groups
         const int key0 = cache_key0(item, w0 + it);
         if (key0 + 127 > item.c_min || (p.win_left >= 0 && key0 < item.c_max - p.win_left && key0 + 127 >= p.sinks)) {
 #pragma unroll
