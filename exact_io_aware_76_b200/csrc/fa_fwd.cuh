@@ -180,6 +180,9 @@ __global__ void __launch_bounds__(384, 1)
       n_iter += n_sink;
     }
   }
+  // Up to 32 sinks in a tile before the window make a narrow step: 32 columns of S, and 32 keys in PV. (A whole step for
+  // a handful of keys cost 11 to 16% of the kernel at windows of 2048 and 1024.)
+  const bool narrow = kSink && n_sink == 1 && p.sinks <= 32;
   const int w_lo[2] = {j_lo[0] - j_begin, j_lo[1] - j_begin};
   auto key_tile = [&](int w) {
     if (!kSink || w < w_sink) return j_begin + w;
@@ -271,22 +274,26 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = mbar_wait(q_full, 0, abort_flag);
       // S_t = Q_t K_j^T : K-major A and B, K (= head dim) advanced 32 B per instruction (16 bf16/fp16 or 32
       // e4m3 elements).
-      auto issue_qk = [&](int t, int s) {
+      auto issue_qk = [&](int t, int s, int step) {
+        uint32_t idesc = idesc_qk;
+        if constexpr (kSink) idesc = narrow && step == w_sink ? idesc_f16(kBF16, 128, 32, false, false) : idesc_qk;
         const uint32_t s_tmem = tmem + t * 128;
         const uint64_t a0 = sdesc_add(q_desc, t * L::kTileBytes), b0 = sdesc_add(k_desc, s * L::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < L::kKSteps; ++kk) {
           const uint32_t koff = (kk / 4) * 16384 + (kk % 4) * 32;
           if (kFP8)
-            umma_ss_f8(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc_qk, kk > 0 ? 1u : 0u);
+            umma_ss_f8(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc, kk > 0 ? 1u : 0u);
           else
-            umma_ss(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc_qk, kk > 0 ? 1u : 0u);
+            umma_ss(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc, kk > 0 ? 1u : 0u);
         }
       };
       // O_t += P_t V_j : A = P_t from TMEM (8 columns per instruction: 16 keys of 16-bit P, or 32 keys of e4m3
       // P), B = V_j MN-major (as many 128-byte key rows per instruction; 64-wide head-dim blocks 16 KB apart).
       // Issued in two halves of 64 keys (with kSplitP the softmax publishes P of keys 0..63 first).
-      auto issue_pv = [&](int t, int s, bool acc, int half) {
+      auto issue_pv = [&](int t, int s, bool acc, int half, int step) {
+        const bool few = kSink && narrow && step == w_sink;
+        if (few && half == 1) return;
         const uint32_t o_tmem = tmem + 256 + t * L::kON;
         const uint32_t p_tmem = tmem + t * 128;
         const uint64_t b0 = sdesc_add(v_desc, s * L::kTileBytes);
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int kHalf = 64 / kKeys;      // instructions per half
 #pragma unroll
         for (int kk = half * kHalf; kk < (half + 1) * kHalf; ++kk) {
+          if (few && kk * kKeys >= 32) break;
           if (kFP8)
             umma_ts_f8(o_tmem, p_tmem + kk * 8, sdesc_add(b0, kk * kKeys * 128), idesc_pv, (acc || kk > 0) ? 1u : 0u);
           else
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after_sync();
         for (int t = 0; t < 2; ++t)
           if (n_kv[t] > 0 && j == w_lo[t]) {
-            issue_qk(t, s);
+            issue_qk(t, s, j);
             umma_commit(&s_full[t]);
           }
         if (!mbar_wait(&v_full[s], ph, abort_flag)) break;
@@ -320,12 +328,12 @@ __global__ void __launch_bounds__(384, 1)
           const int u = j - w_lo[t];  // this tile's local step
           if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          issue_pv(t, s, u > 0, 0);
+          issue_pv(t, s, u > 0, 0, j);
           if (L::kSplitP) {
             if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
           }
-          issue_pv(t, s, true, 1);
+          issue_pv(t, s, true, 1, j);
           umma_commit(&o_full[t]);
           if (u + 1 < n_kv[t]) {
             if (!next_k_ready) {
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(384, 1)
               tc_fence_after_sync();
               next_k_ready = true;
             }
-            issue_qk(t, jn % L::kStages);
+            issue_qk(t, jn % L::kStages, jn);
             umma_commit(&s_full[t]);
           }
         }
@@ -373,6 +381,57 @@ __global__ void __launch_bounds__(384, 1)
       // PV(j-1) completed before S(j) (in-order tensor pipe); waiting keeps the o_full phases in step.
       if (j > 0 && !mbar_wait(&o_full[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after_sync();
+      // Warp-uniform lazy rescale to the running maximum m_cand (TMEM loads/stores are warp-collective).
+      auto rescale_to = [&](float m_cand) {
+        if (!__any_sync(0xffffffffu, m_cand > m + kRescaleLog2)) return;
+        // A row that has not seen a visible key yet (m = -inf) has O = 0 and l = 0; the warp may rescale
+        // because of other rows, and 2^(m - m_cand) would be 2^(-inf + inf) = NaN for it when m_cand is -inf.
+        const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_cand);
+        if (j > 0) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] *= alpha;
+            tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+          }
+          tmem_st_wait();
+        }
+        l *= alpha;
+        m = m_cand;
+      };
+      if constexpr (kSink) {
+        if (narrow && w_lo[t] + j == w_sink) {
+          // The narrow step: every row of the tile sees the sinks, and nothing else of these 32 columns.
+          float x[32];
+          tmem_ld_x32(s_tmem, reinterpret_cast<uint32_t*>(x));
+          float ext = masked;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c >= p.sinks) x[c] = masked;
+            ext = neg_scale ? fminf(ext, x[c]) : fmaxf(ext, x[c]);
+          }
+          rescale_to(fmaxf(m, ext * p.scale_log2));
+          const float m_use = (m == -INFINITY) ? 0.f : m;
+          uint32_t pw[16];
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float p0 = ex2_approx(fmaf(x[c], p.scale_log2, -m_use));
+            const float p1 = ex2_approx(fmaf(x[c + 1], p.scale_log2, -m_use));
+            sum += p0 + p1;
+            pw[c / 2] = pack2<kBF16>(p0, p1);
+          }
+          l += sum;
+          tmem_st_x16(s_tmem, pw);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          if (L::kSplitP) mbar_arrive(&p_half[t]);
+          mbar_arrive(&p_full[t]);
+          continue;
+        }
+      }
       float s[128];
       tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(s));
       const int key0 = key_tile(w_lo[t] + j) * 128;
@@ -407,27 +466,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         ext = fminf(fmin3(mq[0], mq[1], s[124]), fmin3(mq[2], mq[3], fmin3(s[125], s[126], s[127])));
       }
-      const float m_cand = fmaxf(m, ext * p.scale_log2);
-      // Warp-uniform decision: TMEM loads/stores below are warp-collective.
-      const bool rescale = __any_sync(0xffffffffu, m_cand > m + kRescaleLog2);
-      if (rescale) {
-        // A row that has not seen a visible key yet (m = -inf) has O = 0 and l = 0; the warp may rescale
-        // because of other rows, and 2^(m - m_cand) would be 2^(-inf + inf) = NaN for it when m_cand is -inf.
-        const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_cand);
-        if (j > 0) {
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] *= alpha;
-            tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-          }
-          tmem_st_wait();
-        }
-        l *= alpha;
-        m = m_cand;
-      }
+      rescale_to(fmaxf(m, ext * p.scale_log2));
       const float m_use = (m == -INFINITY) ? 0.f : m;
       float sum = 0.f;
       uint32_t pk[L::kPCols];
