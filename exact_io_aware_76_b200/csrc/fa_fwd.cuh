@@ -160,10 +160,9 @@ __global__ void __launch_bounds__(384, 1)
     j_begin = min(j_lo[0], j_lo[1]);
     j_end = max(j_lo[0] + n_kv[0], j_lo[1] + n_kv[1]);
   }
-  // The walk: steps 0 .. n_iter-1, each one key tile; Q tile t takes part in the n_kv[t] steps from w_lo[t] on.
-  // Sink tiles [0, n_sink) before the window are inserted at step w_sink, where tile 1's window begins: tile 0
-  // still has its last window tiles to come there, so both Q tiles keep one unbroken run of steps.
-  int n_iter = j_end - j_begin, n_sink = 0, w_sink = 0;
+  // The walk: steps 0 .. n_iter-1, each one key tile: first the tiles with sinks before the window (both Q tiles take part
+  // in these n_sink steps), then the window's; Q tile t takes part in its n_kv[t] steps of those, from w_lo[t] on.
+  int n_iter = j_end - j_begin, n_sink = 0;
   if constexpr (kSink) {
     if (n_iter > 0) {
       const int n_tiles = (p.sinks + 127) / 128;
@@ -174,20 +173,12 @@ __global__ void __launch_bounds__(384, 1)
           n_kv[t] += j_lo[t] - j_begin;
           j_lo[t] = j_begin;
         }
-      w_sink = (n_kv[0] > 0 && n_kv[1] > 0) ? j_lo[1] - j_begin : 0;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) n_kv[t] += n_kv[t] > 0 ? n_sink : 0;
       n_iter += n_sink;
     }
   }
-  // Up to 32 sinks in a tile before the window make a narrow step: 32 columns of S, and 32 keys in PV. (A whole step for
-  // a handful of keys cost 11 to 16% of the kernel at windows of 2048 and 1024.)
+  // Up to 32 sinks in a tile before the window make a narrow step: 32 columns of S, and 32 keys in PV.
   const bool narrow = kSink && n_sink == 1 && p.sinks <= 32;
-  const int w_lo[2] = {j_lo[0] - j_begin, j_lo[1] - j_begin};
-  auto key_tile = [&](int w) {
-    if (!kSink || w < w_sink) return j_begin + w;
-    return w < w_sink + n_sink ? w - w_sink : j_begin + w - n_sink;
-  };
+  const int w_lo[2] = {n_sink + j_lo[0] - j_begin, n_sink + j_lo[1] - j_begin};
 
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
@@ -237,7 +228,7 @@ __global__ void __launch_bounds__(384, 1)
       int j = 0;  // step of the CTA's walk over key tiles
       for (; j < n_iter; ++j) {
         const int s = j % L::kStages;
-        const int key0 = key_tile(j) * 128;
+        const int key0 = (j < n_sink ? j : j_begin + j - n_sink) * 128;
         if (j >= L::kStages && !mbar_wait(&kv_empty[s], ((j / L::kStages) - 1) & 1, abort_flag)) break;
         mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
         for (int c = 0; c < L::kChunks; ++c)
@@ -276,7 +267,7 @@ __global__ void __launch_bounds__(384, 1)
       // e4m3 elements).
       auto issue_qk = [&](int t, int s, int step) {
         uint32_t idesc = idesc_qk;
-        if constexpr (kSink) idesc = narrow && step == w_sink ? idesc_f16(kBF16, 128, 32, false, false) : idesc_qk;
+        if constexpr (kSink) idesc = narrow && step == 0 ? idesc_f16(kBF16, 128, 32, false, false) : idesc_qk;
         const uint32_t s_tmem = tmem + t * 128;
         const uint64_t a0 = sdesc_add(q_desc, t * L::kTileBytes), b0 = sdesc_add(k_desc, s * L::kTileBytes);
 #pragma unroll
@@ -292,7 +283,7 @@ __global__ void __launch_bounds__(384, 1)
       // P), B = V_j MN-major (as many 128-byte key rows per instruction; 64-wide head-dim blocks 16 KB apart).
       // Issued in two halves of 64 keys (with kSplitP the softmax publishes P of keys 0..63 first).
       auto issue_pv = [&](int t, int s, bool acc, int half, int step) {
-        const bool few = kSink && narrow && step == w_sink;
+        const bool few = kSink && narrow && step == 0;
         if (few && half == 1) return;
         const uint32_t o_tmem = tmem + 256 + t * L::kON;
         const uint32_t p_tmem = tmem + t * 128;
@@ -308,15 +299,15 @@ __global__ void __launch_bounds__(384, 1)
             umma_ts(o_tmem, p_tmem + kk * 8, sdesc_add(b0, kk * kKeys * 128), idesc_pv, (acc || kk > 0) ? 1u : 0u);
         }
       };
-      // Step j serves Q tile t when w_lo[t] <= j < w_lo[t] + n_kv[t]; a tile's first S is issued when the walk
-      // reaches its run of steps, every later one right after its PV.
+      // Step j serves Q tile t when w_lo[t] <= j < w_lo[t] + n_kv[t] (or in the sink steps j < n_sink); the first S of such
+      // a run of steps is issued when the walk reaches it, every later one right after its PV.
       for (int j = 0; ok && j < n_iter; ++j) {
         const int s = j % L::kStages;
         const uint32_t ph = (j / L::kStages) & 1;
         if (!mbar_wait(&k_full[s], ph, abort_flag)) break;
         tc_fence_after_sync();
         for (int t = 0; t < 2; ++t)
-          if (n_kv[t] > 0 && j == w_lo[t]) {
+          if (n_kv[t] > 0 && (j == w_lo[t] || (kSink && j == 0))) {
             issue_qk(t, s, j);
             umma_commit(&s_full[t]);
           }
@@ -324,8 +315,8 @@ __global__ void __launch_bounds__(384, 1)
         const int jn = j + 1;
         bool next_k_ready = false;
         for (int t = 0; t < 2 && ok; ++t) {
-          if (n_kv[t] == 0 || j < w_lo[t] || j >= w_lo[t] + n_kv[t]) continue;
-          const int u = j - w_lo[t];  // this tile's local step
+          if (n_kv[t] == 0 || (j < w_lo[t] && !(kSink && j < n_sink)) || j >= w_lo[t] + n_kv[t]) continue;
+          const int u = (kSink && j < n_sink) ? j : n_sink + j - w_lo[t];  // this tile's local step
           if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
           issue_pv(t, s, u > 0, 0, j);
@@ -335,7 +326,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           issue_pv(t, s, true, 1, j);
           umma_commit(&o_full[t]);
-          if (u + 1 < n_kv[t]) {
+          if ((kSink && j < n_sink) ? j + 1 < n_sink : u + 1 < n_sink + n_kv[t]) {
             if (!next_k_ready) {
               if (!mbar_wait(&k_full[jn % L::kStages], (jn / L::kStages) & 1, abort_flag)) { ok = false; break; }
               tc_fence_after_sync();
@@ -360,7 +351,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t quarter = warp % 4;      // TMEM lanes 32*quarter .. +31
     const int row_in_tile = quarter * 32 + lane;
     const int row = qblk * 256 + t * 128 + row_in_tile;
-    const int nt = n_kv[t];
+    const int nt = n_kv[t] > 0 ? n_sink + n_kv[t] : 0;
     const uint32_t lane_base = tmem + ((quarter * 32) << 16);
     const uint32_t s_tmem = lane_base + t * 128;
     const uint32_t o_tmem = lane_base + 256 + t * L::kON;
@@ -376,65 +367,47 @@ __global__ void __launch_bounds__(384, 1)
     const int tile_row0 = qblk * 256 + t * 128;
     const int all_lo = has_left ? tile_row0 + 127 + off - p.win_left : 0;
     const int all_hi = has_right ? min(p.Sk - 1, tile_row0 + off + right) : p.Sk - 1;
-    for (int j = 0; j < nt; ++j) {
+    int j0 = 0;
+    if constexpr (kSink) {
+      if (narrow && nt > 0) {
+        // The narrow step comes first: every row of the tile sees the sinks, and nothing else of these 32 columns. (Kept
+        // out of the loop below, whose code both warpgroups stream: inside it cost 5% at a window of 2048.)
+        j0 = 1;
+        ok = mbar_wait(&s_full[t], 0, abort_flag);
+        tc_fence_after_sync();
+        float x[32];
+        tmem_ld_x32(s_tmem, reinterpret_cast<uint32_t*>(x));
+        float ext = masked;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          if (c >= p.sinks) x[c] = masked;
+          ext = neg_scale ? fminf(ext, x[c]) : fmaxf(ext, x[c]);
+        }
+        m = ext * p.scale_log2;
+        const float m_use = (m == -INFINITY) ? 0.f : m;
+        uint32_t pw[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float p0 = ex2_approx(fmaf(x[c], p.scale_log2, -m_use));
+          const float p1 = ex2_approx(fmaf(x[c + 1], p.scale_log2, -m_use));
+          l += p0 + p1;
+          pw[c / 2] = pack2<kBF16>(p0, p1);
+        }
+        tmem_st_x16(s_tmem, pw);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        if (L::kSplitP) mbar_arrive(&p_half[t]);
+        mbar_arrive(&p_full[t]);
+      }
+    }
+    for (int j = j0; ok && j < nt; ++j) {
       if (!mbar_wait(&s_full[t], j & 1, abort_flag)) { ok = false; break; }
       // PV(j-1) completed before S(j) (in-order tensor pipe); waiting keeps the o_full phases in step.
       if (j > 0 && !mbar_wait(&o_full[t], (j - 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after_sync();
-      // Warp-uniform lazy rescale to the running maximum m_cand (TMEM loads/stores are warp-collective).
-      auto rescale_to = [&](float m_cand) {
-        if (!__any_sync(0xffffffffu, m_cand > m + kRescaleLog2)) return;
-        // A row that has not seen a visible key yet (m = -inf) has O = 0 and l = 0; the warp may rescale
-        // because of other rows, and 2^(m - m_cand) would be 2^(-inf + inf) = NaN for it when m_cand is -inf.
-        const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_cand);
-        if (j > 0) {
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] *= alpha;
-            tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
-          }
-          tmem_st_wait();
-        }
-        l *= alpha;
-        m = m_cand;
-      };
-      if constexpr (kSink) {
-        if (narrow && w_lo[t] + j == w_sink) {
-          // The narrow step: every row of the tile sees the sinks, and nothing else of these 32 columns.
-          float x[32];
-          tmem_ld_x32(s_tmem, reinterpret_cast<uint32_t*>(x));
-          float ext = masked;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (c >= p.sinks) x[c] = masked;
-            ext = neg_scale ? fminf(ext, x[c]) : fmaxf(ext, x[c]);
-          }
-          rescale_to(fmaxf(m, ext * p.scale_log2));
-          const float m_use = (m == -INFINITY) ? 0.f : m;
-          uint32_t pw[16];
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float p0 = ex2_approx(fmaf(x[c], p.scale_log2, -m_use));
-            const float p1 = ex2_approx(fmaf(x[c + 1], p.scale_log2, -m_use));
-            sum += p0 + p1;
-            pw[c / 2] = pack2<kBF16>(p0, p1);
-          }
-          l += sum;
-          tmem_st_x16(s_tmem, pw);
-          tmem_st_wait();
-          tc_fence_before_sync();
-          if (L::kSplitP) mbar_arrive(&p_half[t]);
-          mbar_arrive(&p_full[t]);
-          continue;
-        }
-      }
       float s[128];
       tmem_ld_x128(s_tmem, reinterpret_cast<uint32_t*>(s));
-      const int key0 = key_tile(w_lo[t] + j) * 128;
+      const int key0 = (kSink && j < n_sink ? j : j_lo[t] + j - n_sink) * 128;
       const bool need_mask =
           (key0 < all_lo && (!kSink || key0 + 127 >= p.sinks)) || key0 + 127 > all_hi;
       if (need_mask) {
@@ -466,7 +439,27 @@ __global__ void __launch_bounds__(384, 1)
         }
         ext = fminf(fmin3(mq[0], mq[1], s[124]), fmin3(mq[2], mq[3], fmin3(s[125], s[126], s[127])));
       }
-      rescale_to(fmaxf(m, ext * p.scale_log2));
+      const float m_cand = fmaxf(m, ext * p.scale_log2);
+      // Warp-uniform decision: TMEM loads/stores below are warp-collective.
+      const bool rescale = __any_sync(0xffffffffu, m_cand > m + kRescaleLog2);
+      if (rescale) {
+        // A row that has not seen a visible key yet (m = -inf) has O = 0 and l = 0; the warp may rescale
+        // because of other rows, and 2^(m - m_cand) would be 2^(-inf + inf) = NaN for it when m_cand is -inf.
+        const float alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_cand);
+        if (j > 0) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] *= alpha;
+            tmem_st_x32(o_tmem + c0, reinterpret_cast<uint32_t*>(o));
+          }
+          tmem_st_wait();
+        }
+        l *= alpha;
+        m = m_cand;
+      }
       const float m_use = (m == -INFINITY) ? 0.f : m;
       float sum = 0.f;
       uint32_t pk[L::kPCols];
