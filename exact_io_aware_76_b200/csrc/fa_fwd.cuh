@@ -265,26 +265,22 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = mbar_wait(q_full, 0, abort_flag);
       // S_t = Q_t K_j^T : K-major A and B, K (= head dim) advanced 32 B per instruction (16 bf16/fp16 or 32
       // e4m3 elements).
-      auto issue_qk = [&](int t, int s, int step) {
-        uint32_t idesc = idesc_qk;
-        if constexpr (kSink) idesc = narrow && step == 0 ? idesc_f16(kBF16, 128, 32, false, false) : idesc_qk;
+      auto issue_qk = [&](int t, int s) {
         const uint32_t s_tmem = tmem + t * 128;
         const uint64_t a0 = sdesc_add(q_desc, t * L::kTileBytes), b0 = sdesc_add(k_desc, s * L::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < L::kKSteps; ++kk) {
           const uint32_t koff = (kk / 4) * 16384 + (kk % 4) * 32;
           if (kFP8)
-            umma_ss_f8(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc, kk > 0 ? 1u : 0u);
+            umma_ss_f8(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc_qk, kk > 0 ? 1u : 0u);
           else
-            umma_ss(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc, kk > 0 ? 1u : 0u);
+            umma_ss(s_tmem, sdesc_add(a0, koff), sdesc_add(b0, koff), idesc_qk, kk > 0 ? 1u : 0u);
         }
       };
       // O_t += P_t V_j : A = P_t from TMEM (8 columns per instruction: 16 keys of 16-bit P, or 32 keys of e4m3
       // P), B = V_j MN-major (as many 128-byte key rows per instruction; 64-wide head-dim blocks 16 KB apart).
       // Issued in two halves of 64 keys (with kSplitP the softmax publishes P of keys 0..63 first).
-      auto issue_pv = [&](int t, int s, bool acc, int half, int step) {
-        const bool few = kSink && narrow && step == 0;
-        if (few && half == 1) return;
+      auto issue_pv = [&](int t, int s, bool acc, int half) {
         const uint32_t o_tmem = tmem + 256 + t * L::kON;
         const uint32_t p_tmem = tmem + t * 128;
         const uint64_t b0 = sdesc_add(v_desc, s * L::kTileBytes);
@@ -292,7 +288,6 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int kHalf = 64 / kKeys;      // instructions per half
 #pragma unroll
         for (int kk = half * kHalf; kk < (half + 1) * kHalf; ++kk) {
-          if (few && kk * kKeys >= 32) break;
           if (kFP8)
             umma_ts_f8(o_tmem, p_tmem + kk * 8, sdesc_add(b0, kk * kKeys * 128), idesc_pv, (acc || kk > 0) ? 1u : 0u);
           else
@@ -301,14 +296,45 @@ __global__ void __launch_bounds__(384, 1)
       };
       // Step j serves Q tile t when w_lo[t] <= j < w_lo[t] + n_kv[t] (or in the sink steps j < n_sink); the first S of such
       // a run of steps is issued when the walk reaches it, every later one right after its PV.
-      for (int j = 0; ok && j < n_iter; ++j) {
+      int j0 = 0;
+      if constexpr (kSink) {
+        if (narrow) {
+          // The narrow step (step 0, stage 0): N = 32 scores and K = 32 weights. (Not a case of the products in the loop:
+          // a branch there slows the one issuing thread, 5% at a window of 2048.)
+          j0 = 1;
+          ok = ok && mbar_wait(&k_full[0], 0, abort_flag);
+          tc_fence_after_sync();
+          for (int t = 0; ok && t < 2; ++t) {
+            if (n_kv[t] == 0) continue;
+            for (int kk = 0; kk < L::kKSteps; ++kk) {
+              const uint32_t koff = (kk / 4) * 16384 + (kk % 4) * 32;
+              umma_ss(tmem + t * 128, sdesc_add(q_desc, t * L::kTileBytes + koff), sdesc_add(k_desc, koff),
+                      idesc_f16(kBF16, 128, 32, false, false), kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[t]);
+          }
+          ok = ok && mbar_wait(&v_full[0], 0, abort_flag);
+          for (int t = 0; ok && t < 2; ++t) {
+            if (n_kv[t] == 0) continue;
+            ok = mbar_wait(&p_full[t], 0, abort_flag) && (!L::kSplitP || mbar_wait(&p_half[t], 0, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+            for (int kk = 0; kk < 2; ++kk)
+              umma_ts(tmem + 256 + t * L::kON, tmem + t * 128 + kk * 8, sdesc_add(v_desc, kk * 2048), idesc_pv,
+                      kk > 0 ? 1u : 0u);
+            umma_commit(&o_full[t]);
+          }
+          umma_commit(&kv_empty[0]);
+        }
+      }
+      for (int j = j0; ok && j < n_iter; ++j) {
         const int s = j % L::kStages;
         const uint32_t ph = (j / L::kStages) & 1;
         if (!mbar_wait(&k_full[s], ph, abort_flag)) break;
         tc_fence_after_sync();
         for (int t = 0; t < 2; ++t)
           if (n_kv[t] > 0 && (j == w_lo[t] || (kSink && j == 0))) {
-            issue_qk(t, s, j);
+            issue_qk(t, s);
             umma_commit(&s_full[t]);
           }
         if (!mbar_wait(&v_full[s], ph, abort_flag)) break;
@@ -319,12 +345,12 @@ __global__ void __launch_bounds__(384, 1)
           const int u = (kSink && j < n_sink) ? j : n_sink + j - w_lo[t];  // this tile's local step
           if (!mbar_wait(L::kSplitP ? &p_half[t] : &p_full[t], u & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          issue_pv(t, s, u > 0, 0, j);
+          issue_pv(t, s, u > 0, 0);
           if (L::kSplitP) {
             if (!mbar_wait(&p_full[t], u & 1, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
           }
-          issue_pv(t, s, true, 1, j);
+          issue_pv(t, s, true, 1);
           umma_commit(&o_full[t]);
           if ((kSink && j < n_sink) ? j + 1 < n_sink : u + 1 < n_sink + n_kv[t]) {
             if (!next_k_ready) {
@@ -332,7 +358,7 @@ __global__ void __launch_bounds__(384, 1)
               tc_fence_after_sync();
               next_k_ready = true;
             }
-            issue_qk(t, jn % L::kStages, jn);
+            issue_qk(t, jn % L::kStages);
             umma_commit(&s_full[t]);
           }
         }
