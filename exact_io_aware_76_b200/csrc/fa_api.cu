@@ -694,7 +694,14 @@ int dispatch_cache(int rows, const CUtensorMap& tk, const CUtensorMap& tv, const
 
 template <int D, bool BF16>
 int launch_append(const AppendParams& p, long long ctas, cudaStream_t stream) {
-  fa::fa_cache_append_kernel<D, BF16><<<(unsigned)ctas, 128, 0, stream>>>(p);
+  const unsigned n = (unsigned)ctas;
+  constexpr int kUnit = D / 64;  // 16-byte pieces per thread of a page of 16
+  switch (p.page) {
+    case 16: fa::fa_cache_append_kernel<D, BF16, kUnit><<<n, 128, 0, stream>>>(p); break;
+    case 32: fa::fa_cache_append_kernel<D, BF16, 2 * kUnit><<<n, 128, 0, stream>>>(p); break;
+    case 64: fa::fa_cache_append_kernel<D, BF16, 4 * kUnit><<<n, 128, 0, stream>>>(p); break;
+    default: fa::fa_cache_append_kernel<D, BF16, 8 * kUnit><<<n, 128, 0, stream>>>(p); break;
+  }
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 }  // namespace

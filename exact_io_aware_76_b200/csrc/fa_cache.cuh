@@ -122,38 +122,47 @@ __device__ __forceinline__ float append_scale(float amax) {
 // One CTA per (sequence, page its new tokens touch, head, K or V): it alone writes that page of that head, so a
 // larger scale can move the page's earlier codes in place. Power-of-two scales make that move exact (but for codes that
 // become subnormal), and cost no precision: e4m3's steps are relative. Bound by bytes for long prompts (read 16 bits,
-// write 8), by latency for single tokens.
-template <int D, bool kBF16>
+// write 8), by latency for single tokens. The page's new tokens stay in registers between the two passes over them
+// (kPasses 16-byte pieces per thread = page * D / 1024), all loads in flight at once: 8 x 1900 tokens, 8 heads of 128,
+// 24 -> 19 us (12 us at the copy rate).
+template <int D, bool kBF16, int kPasses>
 __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;            // 8-element vectors per token
   constexpr int kRows = 128 / kVecs;      // tokens per pass of the CTA
   __shared__ float red[4];
-  long long i = blockIdx.x;
-  const int which = static_cast<int>(i & 1);
-  i >>= 1;
-  const int h = static_cast<int>(i % p.Hkv);
-  i /= p.Hkv;
-  const int touch = static_cast<int>(i % p.n_touch);
-  const int b = static_cast<int>(i / p.n_touch);
+  unsigned n_cta = blockIdx.x;
+  const int which = static_cast<int>(n_cta & 1u);
+  n_cta >>= 1;
+  const int h = static_cast<int>(n_cta % p.Hkv);
+  n_cta /= p.Hkv;
+  const int touch = static_cast<int>(n_cta % p.n_touch);
+  const int b = static_cast<int>(n_cta / p.n_touch);
   const int len = p.lens[b];
   const int count = min(max(p.counts ? p.counts[b] : p.T, 0), min(p.T, max(len, 0)));
   const int first = len - count;
   const int n = first / p.page + touch;
   if (count == 0 || n >= p.max_pages || static_cast<long long>(n) * p.page >= len) return;
-  const int pid = p.table[static_cast<size_t>(b) * p.max_pages + n];
-  if (pid < 0 || pid >= p.num_pages) return;
+  const int pid = __ldg(p.table + static_cast<size_t>(b) * p.max_pages + n);  // (used after the tokens are on their way)
   const int lo = max(first, n * p.page), hi = min(len, n * p.page + p.page);  // positions written here
   const int vec = threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
   const uint16_t* src = static_cast<const uint16_t*>(which ? p.v : p.k) +
                         ((static_cast<size_t>(b) * p.T + (p.T - len + lo)) * p.Hkv + h) * D + vec * 8;
   const size_t stride = static_cast<size_t>(p.Hkv) * D;
+  uint4 v[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + i * kRows < hi - lo) v[i] = __ldg(reinterpret_cast<const uint4*>(src + (r0 + i * kRows) * stride));
+  }
+  if (pid < 0 || pid >= p.num_pages) return;
   uint8_t* codes = (which ? p.v_pages : p.k_pages) + (static_cast<size_t>(pid) * p.Hkv + h) * p.page * D;
   float* sc = (which ? p.v_scale : p.k_scale) + static_cast<size_t>(pid) * p.Hkv + h;
-
+  const int kept = lo - n * p.page;  // earlier tokens of this page
+  const float old = kept > 0 ? *sc : 0.f;
   float amax = 0.f;  // over finite values
-  for (int r = r0; r < hi - lo; r += kRows) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src + r * stride);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a, c;
@@ -167,8 +176,6 @@ __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  const int kept = lo - n * p.page;  // earlier tokens of this page
-  const float old = kept > 0 ? *sc : 0.f;
   __syncthreads();
   amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float now = fmaxf(append_scale(amax), old);
@@ -187,9 +194,11 @@ __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams
   // A power of two (always, unless the caller's earlier scale was none) is divided by exactly as a product.
   const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0u;
   const float inv = 1.f / now;
-  for (int r = r0; r < hi - lo; r += kRows) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src + r * stride);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = r0 + i * kRows;
+    if (r >= hi - lo) break;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
