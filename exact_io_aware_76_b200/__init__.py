@@ -113,8 +113,8 @@ def _dtype_code(t):
 def _check(name, t, dev, shape=None, dtype=None):
     """``t`` must be a contiguous tensor on the CUDA device ``dev`` (and have ``shape`` / ``dtype`` if given)."""
     d = getattr(t, "device", None)
-    if (d == dev and t.is_contiguous() and (shape is None or t.shape == shape)
-            and (dtype is None or t.dtype == dtype) and d.type == "cuda"):
+    if (d == dev and (shape is None or t.shape == shape) and (dtype is None or t.dtype == dtype)
+            and t.is_contiguous() and dev.type == "cuda"):
         return
     if d is None or d.type != "cuda" or d != dev:
         raise ValueError("%s must be a CUDA tensor on %s, got %s" % (name, dev, d))
@@ -205,7 +205,7 @@ def _stream(stream, dev):
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch.cuda.current_stream(dev.index).cuda_stream
     if stream.device != dev:
         raise ValueError("stream is on %s but the tensors are on %s" % (stream.device, dev))
     return stream.cuda_stream
@@ -232,10 +232,13 @@ def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, wind
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
     check_sinks(sinks, dropout_p)
     with _device(dev):
+        made = []
         if out is None:
             out = torch.empty_like(q)
+            made.append(out)
         if lse is None:
-            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
+            made.append(lse)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         shape = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
                  int(bool(causal)), int(window[0]), int(window[1]))
@@ -246,6 +249,7 @@ def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, wind
             rc = lib().fa_fwd_sink(*shape, int(sinks), *sc, _stream(stream, dev))
         else:
             rc = lib().fa_fwd_ex(*shape, *sc, _stream(stream, dev))
+        _used_on(stream, *made)
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_dropout" if dropout_p else "fa_fwd_sink" if sinks else "fa_fwd_ex")
     return out, lse
@@ -262,7 +266,7 @@ def fwd_fp8(q, k, v, causal=False, scale=None, descale=(1.0, 1.0, 1.0), out=None
         if out is None:
             out = torch.empty((B, Sq, H, D), dtype=torch.bfloat16, device=dev)
         if lse is None:
-            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, torch.bfloat16)
         rc = lib().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk,
                               H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
@@ -296,16 +300,18 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
     if stage != -1 and (dropout_p or Hkv != H or tuple(window) != (-1, -1) or sinks):
         raise ValueError("single backward stages are available for plain attention only")
     with _device(dev):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
+        made = [x for x, given in ((q, dq), (k, dk), (v, dv)) if given is None]
+        made = [torch.empty_like(x) for x in made]
+        fresh = iter(made)
+        dq, dk, dv = (next(fresh) if x is None else x for x in (dq, dk, dv))
         if sinks:
             ws_bytes = sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks)
         else:
             ws_bytes = workspace_size(B, Sq, H, D)
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Sq, H, D, dev)
         if workspace is None:
-            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
+            made.append(workspace)
         sc = float(0.0 if scale is None else scale)
         ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
@@ -322,6 +328,7 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
         else:
             rc = lib().fa_bwd_stage(int(stage), *ptrs, B, Sq, Sk, H, D, int(bool(causal)), sc, _dtype_code(q),
                                     *ws_args)
+        _used_on(stream, *made)
     if rc != FA_OK:
         raise FAError(rc, "fa_bwd_sink" if sinks else "fa_bwd")
     return dq, dk, dv
@@ -407,12 +414,12 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, wi
             out = torch.empty_like(q)
             made.append(out)
         if lse is None:
-            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
             made.append(lse)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         ws_bytes = cache_workspace_size(B, Sq, H, Hkv, D)
         if workspace is None:
-            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
             made.append(workspace)
         _check("workspace", workspace, dev)
         if workspace.numel() * workspace.element_size() < ws_bytes:
