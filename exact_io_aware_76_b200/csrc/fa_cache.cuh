@@ -452,7 +452,7 @@ struct CacheSmem {
 // dependent loads is waited for. Pages that no row sees, and page numbers outside the cache, are copied from beyond the
 // tensor's end: the copy engine writes zeros and reads nothing.
 // The factors of a tile's key groups go into a ring of kFac places; kFac = kStages: they are published with K.
-template <int kRows, int kStages, int kFac>
+template <int kRows, int kStages, int kFac, bool kK = true, bool kV = true>
 __device__ __forceinline__ void cache_producer(const CacheParams& p, const CacheRun& run, const CUtensorMap& tm_k,
                                                const CUtensorMap& tm_v, uint8_t* smem_k, uint8_t* smem_v, float* fac,
                                                uint64_t* k_full, uint64_t* v_full, uint64_t* kv_empty,
@@ -516,11 +516,11 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
       // The copies need the page number only; their bytes count towards a phase that the arrival below opens and ends.
       if (tt == u && leads) {
         const int row = cur.row >= 0 ? cur.row : beyond;
-        tma_load_2d(smem_k + s * 16384 + grp * 2048, &tm_k, &k_full[s], 0, row);
-        tma_load_2d(smem_v + s * 16384 + grp * 2048, &tm_v, &v_full[s], 0, row);
+        if (kK) tma_load_2d(smem_k + s * 16384 + grp * 2048, &tm_k, &k_full[s], 0, row);
+        if (kV) tma_load_2d(smem_v + s * 16384 + grp * 2048, &tm_v, &v_full[s], 0, row);
       }
       __syncwarp();
-      if (tt == u) {
+      if (kK && tt == u) {
         const bool valid = cur.row >= 0;
         float* f = fac + (g % kFac) * 24 + grp;
         f[0] = valid ? cur.ks : 1.f;
@@ -530,8 +530,8 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
       __syncwarp();
       if (lane == 0) {
         if (kFac != kStages) mbar_arrive(&fac_full[g % kFac]);
-        mbar_arrive_expect_tx(&k_full[s], 16384);
-        mbar_arrive_expect_tx(&v_full[s], 16384);
+        if (kK) mbar_arrive_expect_tx(&k_full[s], 16384);
+        if (kV) mbar_arrive_expect_tx(&v_full[s], 16384);
       }
     }
     cur = nxt;
@@ -542,9 +542,9 @@ __device__ __forceinline__ void cache_producer(const CacheParams& p, const Cache
     const int issued = ok ? run.count : g;
     for (int i = max(0, issued - kStages); i < issued; ++i) {
       int drain = 0;
-      mbar_wait(&k_full[i % kStages], (i / kStages) & 1, &drain);
+      if (kK) mbar_wait(&k_full[i % kStages], (i / kStages) & 1, &drain);
       drain = 0;
-      mbar_wait(&v_full[i % kStages], (i / kStages) & 1, &drain);
+      if (kV) mbar_wait(&v_full[i % kStages], (i / kStages) & 1, &drain);
     }
   }
 }
@@ -736,8 +736,11 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      cache_producer<R, kStages, kStages>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full, v_full,
-                                          kv_empty, nullptr, abort_flag);
+      cache_producer<R, kStages, kStages, true, false>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full,
+                                                       v_full, kv_empty, nullptr, abort_flag);
+    } else if (warp == 11) {
+      cache_producer<R, kStages, kStages, false, true>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full,
+                                                       v_full, kv_empty, nullptr, abort_flag);
     } else if (warp == 9 && lane == 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
