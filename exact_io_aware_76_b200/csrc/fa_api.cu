@@ -50,6 +50,10 @@ int current_device(int* dev) {
   return d.supported ? FA_OK : FA_ERR_UNSUPPORTED;
 }
 
+// A window bound that hides nothing (or a negative one) becomes -1, so that the kernels' sums of a bound and a row index
+// stay far from overflow whatever the caller passes.
+int window_bound(int w, int Sq, int Sk) { return (w < 0 || w >= (long long)Sq + Sk) ? -1 : w; }
+
 // Opt a kernel into its dynamic shared-memory size once per device.
 template <typename Kernel>
 int ensure_smem_attr(Kernel k, int bytes, int dev, bool* done) {
@@ -357,6 +361,8 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   int dev = 0;
   if ((rc = current_device(&dev))) return rc;
   if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  window_left = window_bound(window_left, Sq, Sk);
+  window_right = window_bound(window_right, Sq, Sk);
   const SinkPlan sp = sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks);
 
   CUtensorMap tq, tk, tv;
@@ -370,8 +376,8 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.win_left = sp.window_left < 0 ? -1 : sp.window_left;
-  p.win_right = window_right < 0 ? -1 : window_right;
+  p.win_left = sp.window_left;
+  p.win_right = window_right;
   p.sinks = sp.sinks;
   p.Sq = Sq;
   p.Sk = Sk;
@@ -430,6 +436,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* out, float* ls
   int dev = 0;
   if ((rc = current_device(&dev))) return rc;
   if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  window_left = window_bound(window_left, Sq, Sk);
+  window_right = window_bound(window_right, Sq, Sk);
 
   CUtensorMap tq, tk, tv;
   if ((rc = make_bshd_map(&tq, q, B, Sq, H, D, kDtypeE4M3, 128))) return rc;
@@ -442,8 +450,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* out, float* ls
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.win_left = window_left < 0 ? -1 : window_left;
-  p.win_right = window_right < 0 ? -1 : window_right;
+  p.win_left = window_left;
+  p.win_right = window_right;
   p.sinks = 0;
   p.Sq = Sq;
   p.Sk = Sk;
@@ -475,8 +483,9 @@ size_t fa_bwd_sink_workspace_size(int B, int Sq, int Sk, int H, int Hkv, int D, 
                                   int window_right, int sinks) {
   if (Hkv < 1 || H < 1 || H % Hkv != 0 || sinks < 0) return 0;
   if (check_common(B, Sq, Sk, H, D, 1.f, FA_F16) != FA_OK) return 0;
-  return bwd_layout(B, Sq, H, D).total +
-         sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks).part_bytes;
+  return bwd_layout(B, Sq, H, D).total + sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_bound(window_left, Sq, Sk),
+                                                   window_bound(window_right, Sq, Sk), sinks)
+                                             .part_bytes;
 }
 
 static int bwd_impl(int stage, const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -493,6 +502,8 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
   int rc = check_common(B, Sq, Sk, H, D, scale, dtype);
   if (rc) return rc;
   const BwdLayout lay = bwd_layout(B, Sq, H, D);
+  window_left = window_bound(window_left, Sq, Sk);
+  window_right = window_bound(window_right, Sq, Sk);
   const SinkPlan sp = sink_plan(B, Sq, Sk, H, Hkv, D, causal, window_left, window_right, sinks);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < lay.total + sp.part_bytes)
@@ -522,8 +533,8 @@ static int bwd_impl(int stage, const void* q, const void* k, const void* v, cons
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.win_left = sp.window_left < 0 ? -1 : sp.window_left;
-  p.win_right = window_right < 0 ? -1 : window_right;
+  p.win_left = sp.window_left;
+  p.win_right = window_right;
   p.sinks = sp.sinks;
   p.sink_tiles = sp.tiles;
   p.sink_pieces = sp.pieces;

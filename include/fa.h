@@ -259,8 +259,8 @@ FA_API size_t fa_cache_workspace_size(int B, int Sq, int H, int Hkv, int D);
  *     included). A non-finite V that some query of the call sees may reach the call's other rows of that K/V head.
  *   - Probabilities reach the PV product with the precision of the output type (relative error 2^-8 or 2^-11); q as it
  *     is, but for elements below 2^-9 of their row's largest (absolute error 2^-17 of that).
- *   - workspace: fa_cache_workspace_size bytes, 256-byte aligned; contents on entry do not matter. Results repeat
- *     bit for bit.
+ *   - workspace: fa_cache_workspace_size bytes, 256-byte aligned; contents on entry do not matter. Calls that may run
+ *     at the same time (two streams, two captured graphs) need a workspace each. Results repeat bit for bit.
  */
 FA_API int fa_cache_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                         const float* v_scale, const int* table, const int* lens, void* out, float* lse, int B, int Sq,

@@ -69,11 +69,11 @@ def values(c, x, b, h, n):
     return out, has
 
 
-def check(q, c, out, lse, left, sinks, scale=None):
+def check(q, c, out, lse, left, sinks, scale=None, only=None):
     B, Sq, H, D = q.shape
     Hkv = c["k_pages"].shape[1]
     tol, floor = (2.0 ** -7, 2.0 ** -12) if q.dtype == torch.bfloat16 else (2.0 ** -9, 2.0 ** -19)
-    for b in range(B):
+    for b in range(B) if only is None else only:
         n = int(c["lens"][b])
         mask = ref.visible(Sq, n, True, (left, -1), sinks, "cuda", shift=n - Sq)
         for g in range(Hkv):
@@ -382,3 +382,77 @@ def test_more_than_32_bits_of_bytes():
     out, lse = fa.fwd_cache(q, **c)
     check(q, c, out, lse, -1, 0)
     assert not c["k_pages"].view(torch.uint8)[:n - 4].any()
+
+
+@pytest.mark.parametrize("longest", [300, 6000])
+def test_more_sequences_than_threads(longest):
+    """The split of the work searches the sequences in blocks: many short ones, without and with long ones between."""
+    g = gen(83)
+    lens = torch.randint(0, 301, (1000,), generator=g, device="cuda").tolist()
+    for b in (0, 383, 384, 767, 768, 999):
+        lens[b] = longest
+    c = make_cache(lens, 1, 64, 16, g)
+    q = torch.randn((1000, 1, 2, 64), generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = fa.fwd_cache(q, **c)
+    check(q, c, out, lse, -1, 0, only=[0, 1, 2, 100, 382, 383, 384, 385, 500, 767, 768, 769, 998, 999])
+    seen = c["lens"] > 0
+    assert torch.isfinite(lse[seen]).all() and torch.isneginf(lse[~seen]).all()
+    alone = fa.fwd_cache(q[500:501], **{**c, "table": c["table"][500:501].contiguous(), "lens": c["lens"][500:501]})
+    assert (out[500] - alone[0][0]).abs().max() <= 2.0 ** -6
+
+
+def test_more_row_blocks_than_threads():
+    g = gen(84)
+    c = make_cache([1100, 1500, 1101], 1, 128, 64, g)
+    q = torch.randn((3, 1100, 32, 128), generator=g, device="cuda").to(torch.float16)
+    out, lse = fa.fwd_cache(q, **c)
+    check(q, c, out, lse, -1, 0)
+
+
+def test_shared_pages_and_two_calls_at_once():
+    """Sequences that share a prefix's pages (and one that has a page twice), and two calls on two streams."""
+    g = gen(85)
+    c = make_cache([1280, 1300, 1500], 2, 128, 64, g)
+    c["table"][1, :18] = c["table"][0, :18]
+    c["table"][2, 3] = c["table"][2, 2]
+    q = torch.randn((3, 2, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+    want = fa.fwd_cache(q, **c)
+    check(q, c, *want, -1, 0)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([fa.fwd_cache(q, **c) for _ in range(3)])
+    torch.cuda.synchronize()
+    for r in got[0] + got[1]:
+        assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
+
+
+def test_one_heavy_token_among_many_light_ones():
+    """An attention sink: one key 11 (in the exponent of e) above 20000 equal ones, whose weights together are what
+    counts: sum 20000 e^-11 = 0.33 against 1. Both kernels keep weights that small."""
+    n, D = 20001, 64
+    for Sq, H in ((1, 8), (1, 16), (1, 32), (40, 4)):
+        for dtype in (torch.bfloat16, torch.float16):
+            page = 64
+            m = -(-n // page)
+            kp = torch.zeros((m, 1, page, D), device="cuda")
+            kp[0, 0, 0, 0] = 1.0
+            vp = torch.zeros((m, 1, page, D), device="cuda")
+            vp[..., 1] = 1.0
+            vp[0, 0, 0, 1] = 0.0
+            c = {"k_pages": kp.to(E4M3), "v_pages": vp.to(E4M3), "k_scale": torch.ones((m, 1), device="cuda"),
+                 "v_scale": torch.ones((m, 1), device="cuda"),
+                 "table": torch.arange(m, device="cuda", dtype=torch.int32)[None].contiguous(),
+                 "lens": torch.tensor([n], dtype=torch.int32, device="cuda")}
+            q = torch.zeros((1, Sq, H, D), device="cuda", dtype=dtype)
+            q[..., 0] = 11.0
+            out, lse = fa.fwd_cache(q, **c, scale=1.0)
+            light = (n - Sq + torch.arange(Sq, device="cuda")).double() * math.exp(-11.0)
+            want = (light / (1 + light))[None, :, None].expand(1, Sq, H)
+            # the light weights share one rounding: a step of the last part (2^-9 / 2^4 of a largest weight of at least
+            # 2^6) against e^-11 = 2^-15.9 of it is 2^-3.1, half of it 6%; the others' parts are finer
+            tol = 0.07 if dtype == torch.bfloat16 and Sq == 1 and H < 32 else 0.03
+            assert ((out[..., 1].double() - want).abs() <= tol * want).all(), (Sq, H, dtype, float(out[0, 0, 0, 1]), float(want[0, 0, 0]))
+            assert (lse.double() - (11.0 + torch.log1p(light))).abs().max() <= 1e-3

@@ -138,3 +138,33 @@ def test_captured_backward_replays_with_its_own_workspace():
         torch.cuda.synchronize()
         assert torch.equal(o2, out) and torch.equal(grads[1], want[1]) and torch.equal(grads[2], want[2])
         check_grad(heads_f64(grads[0], all_heads(1, 2)), heads_f64(want[0], all_heads(1, 2)), "dQ", rtol=1e-3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_bounds_beyond_every_key(D):
+    """Window bounds up to the largest integer hide nothing, with and without sinks, forward and backward."""
+    q, k, v, do = make(1, 500, 400, 2, 1, D, "bf16", 75)
+    big = 2 ** 31 - 1
+    for causal, window in ((True, (big, big)), (False, (big, big)), (False, (30, big))):
+        plain = (-1, -1) if window[0] == big else (30, -1)
+        for sinks in (0, 5):
+            a = fa.fwd(q, k, v, causal=causal, window=window, sinks=sinks)
+            b = fa.fwd(q, k, v, causal=causal, window=plain, sinks=sinks)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            ga = fa.bwd(q, k, v, *a, do, causal=causal, window=window, sinks=sinks)
+            gb = fa.bwd(q, k, v, *a, do, causal=causal, window=plain, sinks=sinks)
+            assert torch.equal(ga[1], gb[1]) and torch.equal(ga[2], gb[2])
+            assert ga[1].any()
+
+
+def test_given_outputs_on_another_stream():
+    q, k, v, do = make(1, 900, 900, 2, 1, 128, "f16", 76)
+    kw = dict(causal=True, window=(100, 0), sinks=6)
+    want = fa.fwd(q, k, v, **kw)
+    gwant = fa.bwd(q, k, v, *want, do, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = fa.fwd(q, k, v, stream=s, **kw)
+    ggot = fa.bwd(q, k, v, *got, do, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(ggot[1], gwant[1]) and torch.equal(ggot[2], gwant[2])
