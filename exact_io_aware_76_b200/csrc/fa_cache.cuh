@@ -415,6 +415,32 @@ __global__ void __launch_bounds__(2 * D) fa_cache_join_kernel(const CacheParams 
 }
 
 // --------------------------------------------------------------------------------------------- shared pieces
+// The issuing warp's products and commits, predicated on the one lane that issues: the warp's control flow stays uniform,
+// so the compiler may keep descriptors and addresses in uniform registers, where these instructions take them from.
+__device__ __forceinline__ void umma_ss_f8_if(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_f8_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A in e5m2 (B in e4m3)
 
 // Few query rows per unit: R = 8, 16 or 32.
@@ -741,57 +767,76 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 11) {
       cache_producer<R, kStages, kStages, false, true>(p, run, tm_k, tm_v, smem + L::kKOff, smem + L::kVOff, fac, k_full,
                                                        v_full, kv_empty, nullptr, abort_flag);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
       constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
-      auto issue_s = [&](int g) {
-        const uint64_t b0 = sdesc_add(k_desc, (g % kStages) * L::kTile);
+      // This warp paces the kernel (traced: 1240 cycles a tile, of which the tensor core works 512): its control flow is
+      // uniform, stages and phases are counted, not divided out, and the barriers that are mostly complete are tested
+      // together and ahead of their use.
+      const uint32_t lead = lane == 0 ? 1u : 0u;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int count = __shfl_sync(0xffffffffu, run.count, 0);
+      auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+      auto issue_s = [&](uint32_t buf, int s) {
+        const uint64_t b0 = sdesc_add(k_desc, s * L::kTile);
+        const uint32_t d = tm + buf * 128;
 #pragma unroll
         for (int q = 0; q < kQPass; ++q)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            umma_ss_f8(tmem + (g & 1) * 128, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
-                       id_s | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&s_full[g & 1]);
+            umma_ss_f8_if(lead, d, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
+                          id_s | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
+        umma_commit_if(lead, &s_full[buf]);
       };
       CacheWalk<R> walk;
       walk.start(p, run.first);
       bool ok = true;
-      for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
-        const int left = min(run.count - g, walk.item.n - walk.at.w);  // tiles of this unit in the run
-        ok = mbar_wait(q_ready, unit & 1, abort_flag) &&
-             mbar_wait(&k_full[g % kStages], (g / kStages) & 1, abort_flag);
+      int s = 0;          // stage of tile g
+      uint32_t ph = 0;    // phase of its barriers
+      for (int g = 0, unit = 0; ok && g < count; ++unit) {
+        const int left = __shfl_sync(0xffffffffu, min(count - g, walk.item.n - walk.at.w), 0);  // the unit's, in the run
+        ok = all(mbar_wait(q_ready, unit & 1, abort_flag) && mbar_wait(&k_full[s], ph, abort_flag));
         if (!ok) break;
         tc_fence_after_sync();
-        issue_s(g);
+        issue_s(g & 1, s);
         for (int it = 0; it < left; ++it, ++g) {
-          const int s = g % kStages;
-          if (it + 1 < left) {
+          const int s1 = s + 1 == kStages ? 0 : s + 1;
+          const uint32_t ph1 = s1 == 0 ? ph ^ 1u : ph, buf = g & 1, pp = (g >> 1) & 1;
+          const bool more = it + 1 < left;
+          const bool v_ok = mbar_try_wait(&v_clean[s], ph), k_ok = !more || mbar_try_wait(&k_full[s1], ph1);
+          const bool p_ok = mbar_test_wait(&p_full[buf], pp);
+          if (more) {
             // Into the other buffer: the product that read the weights there was issued before.
-            if (!mbar_wait(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1, abort_flag)) { ok = false; break; }
+            if (!all(k_ok || mbar_wait(&k_full[s1], ph1, abort_flag))) { ok = false; break; }
             tc_fence_after_sync();
-            issue_s(g + 1);
+            issue_s(buf ^ 1u, s1);
           }
-          if (!mbar_wait(&v_clean[s], (g / kStages) & 1, abort_flag)) { ok = false; break; }
-          if (!mbar_wait(&p_full[g & 1], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!all((p_ok || mbar_wait(&p_full[buf], pp, abort_flag)) && (v_ok || mbar_wait(&v_clean[s], ph, abort_flag)))) {
+            ok = false;
+            break;
+          }
           tc_fence_after_sync();
           const uint64_t b0 = sdesc_add(v_desc, s * L::kTile);
+          const uint32_t d = tm + 256 + buf * 128, a = tm + buf * 128;
 #pragma unroll
           for (int q = 0; q < kPPass; ++q)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts_f8(tmem + 256 + (g & 1) * 128, tmem + (g & 1) * 128 + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
-                         id_o | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (it > 1 || q > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&kv_empty[s]);
+              umma_ts_f8_if(lead, d, a + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
+                            id_o | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u),
+                            (it > 1 || q > 0 || kk > 0) ? 1u : 0u);
+          umma_commit_if(lead, &kv_empty[s]);
+          s = s1;
+          ph = ph1;
         }
-        umma_commit(unit_done);
-        if (ok && g < run.count) walk.advance(p, left);
+        umma_commit_if(lead, unit_done);
+        if (ok && g < count) walk.advance(p, left);
       }
-      umma_commit(mma_done);
+      umma_commit_if(lead, mma_done);
       int drain = 0;
       mbar_wait(mma_done, 0, &drain);
     } else if (warp == 10) {
