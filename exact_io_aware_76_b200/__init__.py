@@ -32,7 +32,8 @@ STATUS_NAMES = {0: "FA_OK", -1: "FA_ERR_INVALID", -2: "FA_ERR_UNSUPPORTED", -3: 
                 -4: "FA_ERR_TIMEOUT", -5: "FA_ERR_WORKSPACE"}
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_dropout", "fa_fwd_sink", "fa_bwd_dropout", "fa_bwd",
            "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace_size", "fa_bwd_stage", "fa_bwd_noalloc",
-           "fa_bwd_workspace_size", "fa_cache_append", "fa_cache_fwd", "fa_cache_workspace_size", "fa_status_string", "fa_device_status")
+           "fa_bwd_workspace_size", "fa_cache_append", "fa_cache_fwd", "fa_cache_workspace_size", "fa_status_string",
+           "fa_device_status")
 
 _lib = None
 
@@ -361,7 +362,7 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, counts=N
 
     k, v [B, T, Hkv, D] fp16 or bf16; k_pages, v_pages [num_pages, Hkv, page, D] float8_e4m3fn; k_scale, v_scale
     [num_pages, Hkv] fp32; table [B, max_pages] and lens [B] int32: page numbers, and lengths with the new tokens.
-    The last ``counts[b]`` (int32 [B]; default T) of sequence b's rows are its new tokens. The cache is changed in place."""
+    The last ``counts[b]`` (int32 [B]; default T) of sequence b's rows are its new tokens. Changes the cache in place."""
     import torch
 
     dev = getattr(k, "device", None)

@@ -4,8 +4,9 @@
 // K and for V (value = code * scale); a table [B, max_pages] of page numbers and a length per sequence. A page of one
 // head is contiguous (page * D bytes), so it arrives as one TMA box, and 128 keys of a head are 128 / page boxes.
 //
-// Few query rows (decoding): attention without converting the cache. K and V stay e4m3 all the way into the tensor core (tcgen05 kind::f8f6f4);
-// it is the other operand that is brought to 8 bits, without loss: a 16-bit number has 8 (bf16) or 11 (fp16)
+// Few query rows (decoding): attention without converting the cache. K and V stay e4m3 all the way into the tensor core
+// (tcgen05 kind::f8f6f4); it is the other operand that is brought to 8 bits, without loss: a 16-bit number has 8 (bf16) or
+// 11 (fp16)
 // significant bits and an e4m3 number 4, so q = q1 + q2 (+ q3) with q1 = e4m3(q), q2 = e4m3(q - q1) and, for fp16,
 // a third part for the 3 bits left is exact as long as the parts stay in range (split_f16x2).
 // Each query row is first scaled by a power of two that brings its largest element to [128, 256); elements below
@@ -25,8 +26,9 @@
 // Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
 // tiles, and before them the tiles with sinks). All units' tiles are laid end to end, each unit's with a few places
 // before them for what a unit costs by itself (kCacheUnitCost), and every CTA takes an equal run of places, whatever the
-// lengths are, so neither one long sequence nor many short ones load the SMs unevenly. Units cut by a run's border leave fp32 partial sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so
-// results repeat bit for bit.
+// lengths are, so neither one long sequence nor many short ones load the SMs unevenly (32 sequences of 100 to 8000
+// tokens: 110 us with places for tiles only, 73 us with 3 more per unit). Units cut by a run's border leave fp32 partial
+// sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so results repeat bit for bit.
 #pragma once
 #include "fa_fwd.cuh"
 
@@ -473,11 +475,11 @@ struct CacheSmem {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
-// The TMA warp: walks the run's tiles, a lane per 16-key group, four tiles per batch. The page numbers of the batch
-// after next and the scales of the next batch are loaded while this batch's copies are issued, so that neither of the two
-// dependent loads is waited for. Pages that no row sees, and page numbers outside the cache, are copied from beyond the
-// tensor's end: the copy engine writes zeros and reads nothing.
-// The factors of a tile's key groups go into a ring of kFac places; kFac = kStages: they are published with K.
+// A copying warp (K, V or both): walks the run's tiles, a lane per 16-key group, four tiles per batch. The page numbers
+// of the batch after next and the scales of the next batch are loaded while this batch's copies are issued, so that
+// neither of the two dependent loads is waited for. Pages that no row sees, and page numbers outside the cache, are copied
+// from beyond the tensor's end: the copy engine writes zeros and reads nothing. The factors of a tile's key groups go into a
+// ring of kFac places; kFac = kStages: they are published with K.
 template <int kRows, int kStages, int kFac, bool kK = true, bool kV = true>
 __device__ __forceinline__ void cache_producer(const CacheParams& p, const CacheRun& run, const CUtensorMap& tm_k,
                                                const CUtensorMap& tm_v, uint8_t* smem_k, uint8_t* smem_v, float* fac,
@@ -688,12 +690,15 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 // scores are added across lanes, and their rows of O at the end. The other copies share out the tile's 128 keys: each
 // warp has 32, and where copies are left its lanes take 16 each; a copy has a running maximum, sum and rows of O of its
 // own, and weights of 0 for the others' keys. Nothing else is exchanged until the copies are joined, once, at the end of
-// the unit. (One product with all parts instead of one per part: 32 x 32768 tokens, 64 query heads on 8, bf16:
-// 505 -> 427 us; an M = N = 128, K = 32 product of 8-bit operands takes 115 to 140 cycles here, so the products were the bound.)
+// the unit. Measured at 32 x 32768 tokens, 64 query heads on 8, bf16 (2.15 GB: 328 us at the copy rate): one product
+// per part 505 us; one product with all parts 427; two softmax warpgroups 398; each score computed by one lane 383; two
+// warps copying 388, but 526 -> 420 with pages of 16; the issuing warp uniform 371 (91% of the copy rate; 429 in a loop
+// of seconds, where the power cap holds the SMs at 1.43 GHz and the same copy takes 335). What bounds it then is the chain
+// issue -> scores -> weights -> issue, 1240 cycles a tile.
 //
 // Warps: 0-3 and 4-7 softmax of the even and the odd tiles of the run, each warpgroup with its own S and O (so its own
 // maxima and sums too, joined with the others at the end): two tiles are in work at any time, and a warpgroup's
-// latencies have two tiles' time to pass in. 8 TMA, 9 MMA, 10 cleaner (see cache_cleaner), 11 idle.
+// latencies have two tiles' time to pass in. 8 and 11 copy K and V (TMA), 9 MMA, 10 cleaner (see cache_cleaner).
 // TMEM columns: S of both [0,128) and [128,256), O [256,384) and [384,512); the parts of P overwrite their S, 32 columns
 // each. The MMA order is S(g+1), PV(g), S(g+2), ..., so when S(g) has arrived PV(g-2), the last product of that
 // warpgroup, is complete: O may be rescaled without a further wait.
@@ -1136,7 +1141,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (whole) {
               const int rr = t.row0 + ro, qi = rr / p.group, h = hk * p.group + rr % p.group;
-              uint16_t* dst = static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + cb + col;
+              uint16_t* dst =
+                  static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(t.b) * p.Sq + qi) * p.H + h) * D + cb + col;
               *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kBF16>(sum.x, sum.y), pack2<kBF16>(sum.z, sum.w));
             } else {
               *reinterpret_cast<float4*>(p.part_o + (slot0 + ro) * D + cb + col) = sum;
@@ -1163,7 +1169,8 @@ __global__ void __launch_bounds__(384, 1)
 // turn each arrived tile of V into an fp16 tile (exact), the weights are fp16 in one rounding, and PV is a 16-bit
 // product. K stays e4m3: q's parts are made once per unit, and the parts' products take as long as one 16-bit product
 // (bf16). (Weights in parts: 788 us for 4096 tokens of a prompt of 8192, 32 heads on 8, bf16; K and V converted: 644 to
-// 738 us; this: 511 us, where the forward on 16-bit K and V of that length takes 399 us.) V rows that no query sees are written as 0.
+// 738 us; this: 511 us, where the forward on 16-bit K and V of that length takes 399 us. Traced, a pair of tiles takes
+// 4480 cycles: the issue of its 32 products 2800, a softmax 2300 beside them.) V rows that no query sees are written as 0.
 //
 // Warps: 0-3 and 4-7 softmax of Q tiles 0 and 1, 8 TMA, 9 MMA, 10-11 conversion. TMEM columns: S0 [0,128), S1 [128,256),
 // O0 [256,256+D), O1 [384,384+D); P_t overwrites the first 64 columns of S_t.

@@ -88,9 +88,11 @@ def check(q, c, out, lse, left, sinks, scale=None, only=None):
                 p, o_r, l_r = ref.forward(q[b, :, h].double(), k, v, m, scale)
                 blind = ~m.any(1)
                 assert not o[blind].any() and torch.isneginf(ls[blind]).all()
-                assert torch.isfinite(ls[~blind]).all() and (ls - l_r)[~blind].abs().max() <= 1e-3 if (~blind).any() else 1
+                if (~blind).any():
+                    assert torch.isfinite(ls[~blind]).all() and (ls - l_r)[~blind].abs().max() <= 1e-3
                 seen = v * m.any(0)[:, None]
-                ulp = 2.0 ** (torch.floor(torch.log2(o_r.abs().clamp(min=2.0 ** -14))) - (8 if q.dtype == torch.bfloat16 else 11))
+                exponent = torch.floor(torch.log2(o_r.abs().clamp(min=2.0 ** -14)))
+                ulp = 2.0 ** (exponent - (8 if q.dtype == torch.bfloat16 else 11))
                 bound = tol * (p @ v.abs()) + 4 * floor * p.amax(-1, keepdim=True) * seen.norm(dim=0)[None] + ulp
                 bad = ~((o - o_r).abs() <= bound)
                 assert not bad.any(), (b, h, int(bad.sum()), float(((o - o_r).abs() / bound).max()))
@@ -454,5 +456,5 @@ def test_one_heavy_token_among_many_light_ones():
             # the light weights share one rounding: a step of the last part (2^-9 / 2^4 of a largest weight of at least
             # 2^6) against e^-11 = 2^-15.9 of it is 2^-3.1, half of it 6%; the others' parts are finer
             tol = 0.07 if dtype == torch.bfloat16 and Sq == 1 and H < 32 else 0.03
-            assert ((out[..., 1].double() - want).abs() <= tol * want).all(), (Sq, H, dtype, float(out[0, 0, 0, 1]), float(want[0, 0, 0]))
+            assert ((out[..., 1].double() - want).abs() <= tol * want).all(), (Sq, H, dtype)
             assert (lse.double() - (11.0 + torch.log1p(light))).abs().max() <= 1e-3
