@@ -112,10 +112,11 @@ def _dtype_code(t):
 
 
 def _check(name, t, dev, shape=None, dtype=None):
-    """``t`` must be a contiguous tensor on the CUDA device ``dev`` (and have ``shape`` / ``dtype`` if given)."""
+    """``t`` must be a contiguous tensor on ``dev``, which the callers have found to be a CUDA device (and have
+    ``shape`` / ``dtype`` if given)."""
     d = getattr(t, "device", None)
     if (d == dev and (shape is None or t.shape == shape) and (dtype is None or t.dtype == dtype)
-            and t.is_contiguous() and dev.type == "cuda"):
+            and t.is_contiguous()):
         return
     if d is None or d.type != "cuda" or d != dev:
         raise ValueError("%s must be a CUDA tensor on %s, got %s" % (name, dev, d))
