@@ -126,12 +126,12 @@ __device__ __forceinline__ float append_scale(float amax) {
 // become subnormal), and cost no precision: e4m3's steps are relative. Bound by bytes for long prompts (read 16 bits,
 // write 8), by latency for single tokens. The page's new tokens stay in registers between the two passes over them
 // (kPasses 16-byte pieces per thread = page * D / 1024), all loads in flight at once: 8 x 1900 tokens, 8 heads of 128,
-// 24 -> 19 us (12 us at the copy rate).
+// 24 -> 19 us; magnitudes compared as packed patterns: 16 us (12 us at the copy rate; 64 x 2048 tokens: 144 us, 0.86 of it).
 template <int D, bool kBF16, int kPasses>
 __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;            // 8-element vectors per token
   constexpr int kRows = 128 / kVecs;      // tokens per pass of the CTA
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   unsigned n_cta = blockIdx.x;
   const int which = static_cast<int>(n_cta & 1u);
   n_cta >>= 1;
@@ -161,25 +161,33 @@ __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams
   float* sc = (which ? p.v_scale : p.k_scale) + static_cast<size_t>(pid) * p.Hkv + h;
   const int kept = lo - n * p.page;  // earlier tokens of this page
   const float old = kept > 0 ? *sc : 0.f;
-  float amax = 0.f;  // over finite values
+  // The largest magnitude, as 16-bit patterns two at a time (patterns of magnitudes order as the magnitudes do). Where
+  // the page's new tokens hold an infinity or a NaN the patterns of those are left out in a second round.
+  constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+  for (int round = 0; round < 2; ++round) {
+    uint32_t mx = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a, c;
-      unpack2<kBF16>(w[e], a, c);
-      a = fabsf(a);
-      c = fabsf(c);
-      amax = fmaxf(amax, a < INFINITY ? a : 0.f);
-      amax = fmaxf(amax, c < INFINITY ? c : 0.f);
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t a = w[e] & 0x7fff7fffu;
+        if (round == 1) a = ((a & 0xffffu) < kInf ? a & 0xffffu : 0u) | ((a >> 16) < kInf ? a & 0xffff0000u : 0u);
+        mx = __vmaxu2(mx, a);
+      }
     }
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (round == 1) __syncthreads();  // the first round's values are read
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    top = max(max(red[0], red[1]), max(red[2], red[3]));
+    if (top < kInf) break;
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float amax, unused;
+  unpack2<kBF16>(top, amax, unused);
   const float now = fmaxf(append_scale(amax), old);
   if (kept > 0 && now != old) {
     const float f = old / now;
