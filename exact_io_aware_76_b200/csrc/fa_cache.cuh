@@ -639,8 +639,8 @@ template <int kParts, int kStack>
 __device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t* code) {
 #pragma unroll
   for (int q = 0; q < kParts; ++q) {
-    constexpr uint32_t kUp[4] = {0x3c003c00u, 0x4c004c00u, 0x5c005c00u, 0x6c006c00u};    // 1, 2^4, 2^8, 2^12
-    constexpr uint32_t kDown[4] = {0x3c003c00u, 0x2c002c00u, 0x1c001c00u, 0x0c000c00u};  // 1, 2^-4, 2^-8, 2^-12
+    constexpr uint32_t kUp[3] = {0x3c003c00u, 0x4c004c00u, 0x5c005c00u};    // 1, 2^4, 2^8
+    constexpr uint32_t kDown[3] = {0x3c003c00u, 0x2c002c00u, 0x1c001c00u};  // 1, 2^-4, 2^-8
     const uint32_t up = q % kStack ? mul_f16x2(h, kUp[q % kStack]) : h;
     if (part_is_e5m2(q, kStack)) {
       code[q] = e5m2x2_from_f16x2(up);
@@ -702,7 +702,7 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 // per part 505 us; one product with all parts 427; two softmax warpgroups 398; each score computed by one lane 383; two
 // warps copying 388, but 526 -> 420 with pages of 16; the issuing warp uniform 371 (91% of the copy rate; 429 in a loop
 // of seconds, where the power cap holds the SMs at 1.43 GHz and the same copy takes 335). What bounds it then is the chain
-// issue -> scores -> weights -> issue, 1240 cycles a tile.
+// issue -> scores -> weights -> issue, 1240 cycles a tile as traced (the trace's own stores included).
 //
 // Warps: 0-3 and 4-7 softmax of the even and the odd tiles of the run, each warpgroup with its own S and O (so its own
 // maxima and sums too, joined with the others at the end): two tiles are in work at any time, and a warpgroup's
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
-      // This warp paces the kernel (traced: 1240 cycles a tile, of which the tensor core works 512): its control flow is
+      // This warp paces the kernel (8 products a tile, 72 cycles each, and as long again in waits): its control flow is
       // uniform, stages and phases are counted, not divided out, and the barriers that are mostly complete are tested
       // together and ahead of their use.
       const uint32_t lead = lane == 0 ? 1u : 0u;
