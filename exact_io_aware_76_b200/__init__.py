@@ -169,6 +169,11 @@ def check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B,
             raise ValueError("workspace must hold at least %d bytes" % ws_bytes)
 
 
+def _bound(w):
+    """A window bound as the library's 32-bit integer; one beyond it hides nothing, as the largest does."""
+    return max(-1, min(int(w), 2 ** 31 - 1))
+
+
 def check_sinks(sinks, dropout_p):
     if int(sinks) != sinks or not 0 <= sinks < 2 ** 31:
         raise ValueError("sinks must be a number of keys (a 32-bit integer >= 0), got %r" % (sinks,))
@@ -243,7 +248,7 @@ def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, wind
             made.append(lse)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         shape = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
-                 int(bool(causal)), int(window[0]), int(window[1]))
+                 int(bool(causal)), _bound(window[0]), _bound(window[1]))
         sc = (float(0.0 if scale is None else scale), _dtype_code(q))
         if dropout_p:
             rc = lib().fa_fwd_dropout(*shape, *sc, float(dropout_p), int(seed), int(offset), _stream(stream, dev))
@@ -271,7 +276,7 @@ def fwd_fp8(q, k, v, causal=False, scale=None, descale=(1.0, 1.0, 1.0), out=None
             lse = q.new_empty((B, H, Sq), dtype=torch.float32)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, torch.bfloat16)
         rc = lib().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk,
-                              H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
+                              H, Hkv, D, int(bool(causal)), _bound(window[0]), _bound(window[1]),
                               float(0.0 if scale is None else scale), float(descale[0]), float(descale[1]),
                               float(descale[2]), _stream(stream, dev))
     if rc != FA_OK:
@@ -285,8 +290,8 @@ def workspace_size(B, Sq, H, D):
 
 def sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks):
     """Bytes of workspace the backward with ``sinks`` needs."""
-    return int(lib().fa_bwd_sink_workspace_size(B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]),
-                                                int(window[1]), int(sinks)))
+    return int(lib().fa_bwd_sink_workspace_size(B, Sq, Sk, H, Hkv, D, int(bool(causal)), _bound(window[0]),
+                                                _bound(window[1]), int(sinks)))
 
 
 def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None,
@@ -315,17 +320,18 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
             workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
             made.append(workspace)
         sc = float(0.0 if scale is None else scale)
+        bounds = (_bound(window[0]), _bound(window[1]))
         ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
         ws_args = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev))
         if dropout_p:
-            rc = lib().fa_bwd_dropout(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
-                                      sc, _dtype_code(q), float(dropout_p), int(seed), int(offset), *ws_args)
+            rc = lib().fa_bwd_dropout(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), *bounds, sc,
+                                      _dtype_code(q), float(dropout_p), int(seed), int(offset), *ws_args)
         elif sinks:
-            rc = lib().fa_bwd_sink(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]),
-                                   int(sinks), sc, _dtype_code(q), *ws_args)
+            rc = lib().fa_bwd_sink(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), *bounds, int(sinks), sc,
+                                   _dtype_code(q), *ws_args)
         elif stage == -1:
-            rc = lib().fa_bwd_ex(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), int(window[0]), int(window[1]), sc,
+            rc = lib().fa_bwd_ex(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), *bounds, sc,
                                  _dtype_code(q), *ws_args)
         else:
             rc = lib().fa_bwd_stage(int(stage), *ptrs, B, Sq, Sk, H, D, int(bool(causal)), sc, _dtype_code(q),
@@ -428,7 +434,7 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, wi
             raise ValueError("workspace must hold at least %d bytes" % ws_bytes)
         rc = lib().fa_cache_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
                                 v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                B, Sq, H, Hkv, D, num_pages, page, max_pages, int(window_left), int(sinks),
+                                B, Sq, H, Hkv, D, num_pages, page, max_pages, _bound(window_left), int(sinks),
                                 float(0.0 if scale is None else scale), _dtype_code(q), workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream(stream, dev))
         _used_on(stream, *made)

@@ -123,3 +123,12 @@ def test_binding_refuses_bad_tokens(fake_lib, over):
     with pytest.raises((ValueError, TypeError)):
         fa.cache_append(a["k"], a["v"], **cache(), counts=a["counts"])
     assert fake_lib.calls == []
+
+
+@pytest.mark.parametrize("left,passed", [(130, 130), (2 ** 32 + 130, 2 ** 31 - 1), (-1, -1), (-2 ** 32 + 130, -1)])
+def test_windows_past_32_bits_stay_open(fake_lib, monkeypatch, left, passed):
+    seen = []
+    monkeypatch.setattr(fake_lib, "fa_cache_fwd", lambda *a: seen.append(a) or 0, raising=False)
+    fa.fwd_cache(T((3, 1, 4, 64)), **cache(), window_left=left, sinks=5, out=T((3, 1, 4, 64)), lse=T((3, 4, 1), F32),
+                 workspace=T((1024,), torch.uint8))
+    assert seen[0][17:19] == (passed, 5)

@@ -47,3 +47,9 @@ def test_binding_refuses_sinks_with_dropout():
     fa.check_sinks(4, 0.0)
     with pytest.raises(ValueError):
         fa.check_sinks(4, 0.1)
+
+
+@pytest.mark.parametrize("left", [4199, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 130, -1, -2 ** 32 + 130])
+def test_bounds_past_32_bits_hide_nothing(left):
+    plain = fa.workspace_size(1, 4200, 1, 128)
+    assert fa.sink_workspace_size(1, 4200, 4200, 1, 1, 128, True, (left, 0), 3) == plain
