@@ -728,7 +728,7 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
   if (rc) return rc;
   if ((double)B * T * Hkv * D > 4.0e12) return FA_ERR_INVALID;
   AppendParams p;
-  p.n_touch = (T - 1 + page - 1) / page + 1;
+  p.n_touch = (T - 1) / page + ((T - 1) % page != 0) + 1;
   if (p.n_touch > max_pages) p.n_touch = max_pages;
   const double ctas = 2.0 * B * Hkv * p.n_touch;
   if (ctas > 2147483647.0) return FA_ERR_INVALID;

@@ -126,7 +126,8 @@ __device__ __forceinline__ float append_scale(float amax) {
 // become subnormal), and cost no precision: e4m3's steps are relative. Bound by bytes for long prompts (read 16 bits,
 // write 8), by latency for single tokens. The page's new tokens stay in registers between the two passes over them
 // (kPasses 16-byte pieces per thread = page * D / 1024), all loads in flight at once: 8 x 1900 tokens, 8 heads of 128,
-// 24 -> 19 us; magnitudes compared as packed patterns: 16 us (12 us at the copy rate; 64 x 2048 tokens: 144 us, 0.86 of it).
+// 24 -> 19 us; magnitudes compared as packed patterns: 16 us (12 us at the copy rate; 64 x 2048 tokens: 144 us, 0.86
+// of it).
 template <int D, bool kBF16, int kPasses>
 __global__ void __launch_bounds__(128) fa_cache_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;            // 8-element vectors per token
@@ -637,6 +638,7 @@ __device__ __forceinline__ void q_row_scale(uint32_t amax_bits, float& mul, floa
 // them adds to the first one's row, unscaled, in e5m2, which reaches down to 2^-16.
 template <int kParts, int kStack>
 __device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t* code) {
+  static_assert(kParts <= 3, "a factor for every part");
 #pragma unroll
   for (int q = 0; q < kParts; ++q) {
     constexpr uint32_t kUp[3] = {0x3c003c00u, 0x4c004c00u, 0x5c005c00u};    // 1, 2^4, 2^8
