@@ -473,8 +473,8 @@ struct CacheSmem {
   static constexpr int kXOff = kVOff + kStages * kTile;
   static constexpr int kXBytes = 8 * R * (kJoinCols + 4) * 4;
   static constexpr int kFacOff = kXOff + kXBytes;    // per stage: k factor, log2 v scale, 1 / v scale of 8 key groups
-  static constexpr int kMlOff = kFacOff + kStages * 96;  // row factors [32], m and l per lane [2][256]
-  static constexpr int kBarOff = kMlOff + (32 + 512) * 4;
+  static constexpr int kMlOff = kFacOff + kStages * 96;  // row factors [2][32], m and l per lane [2][256]
+  static constexpr int kBarOff = kMlOff + (64 + 512) * 4;
   static constexpr int kNumBars = 4 * kStages + 8;
   static constexpr int kScanOff = kBarOff + kNumBars * 8;
   static constexpr int kMiscOff = kScanOff + static_cast<int>(sizeof(CacheScan));
@@ -735,8 +735,8 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* unit_done = s_full + 6;       // a unit's products complete
   uint64_t* mma_done = s_full + 7;
   float* fac = reinterpret_cast<float*>(smem + L::kFacOff);
-  float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [32]
-  float* q_m = row_back + 32;                                     // [256 lanes]
+  float* row_back = reinterpret_cast<float*>(smem + L::kMlOff);  // [parity of the unit][32]
+  float* q_m = row_back + 64;                                     // [256 lanes]
   float* q_l = q_m + 256;                                         // [256 lanes]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
@@ -890,7 +890,10 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < kVec; ++i) v[i] = src[i];
         }
       };
-      auto place_q = [&]() {
+      // The row factors have two places, by the unit's parity: a warp may place unit u + 1's q while another still has to
+      // read unit u's factors (a unit's last scores can be complete before every warp has begun it). The same place is
+      // written again with unit u + 2's q, when every warp has passed unit u's joins and so read its factors.
+      auto place_q = [&](int unit) {
         uint32_t amax = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) amax = q_amax8<kBF16>(v[i], amax);
@@ -899,7 +902,7 @@ __global__ void __launch_bounds__(384, 1)
         float mul, back;
         q_row_scale(amax, mul, back);
         if (row_q < R) {
-          if (piece == 0) row_back[row_q] = back * p.scale_log2;
+          if (piece == 0) row_back[(unit & 1) * 32 + row_q] = back * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             uint2 part[kQPass * kStack];
@@ -923,13 +926,13 @@ __global__ void __launch_bounds__(384, 1)
       CacheWalk<R> walk;
       walk.start(p, run.first);
       load_q(walk.item, walk.at.hk);
-      place_q();
+      place_q(0);
       bool ok = join();
       for (int g = 0, unit = 0; ok && g < run.count; ++unit) {
         const CacheItem t = walk.item;
         const int hk = walk.at.hk, w0 = walk.at.w;
         const int left = min(run.count - g, t.n - w0);
-        const float c_row = row_back[r];
+        const float c_row = row_back[(unit & 1) * 32 + r];
         const int row = t.row0 + min(r, t.rows - 1);
         const int aligned = t.c0 + row / p.group;
         const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
@@ -1084,7 +1087,7 @@ __global__ void __launch_bounds__(384, 1)
         if (more) {
           // (the last tile's scores may be the other warpgroup's)
           if (!mbar_wait(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
-          place_q();
+          place_q(unit + 1);
         }
         if (!join()) { ok = false; break; }
         float m_all = -INFINITY, l_all = 0.f;

@@ -1,0 +1,32 @@
+"""The paged e4m3 cache where its kernels could go wrong without a sign: runs of short units in one CTA, factors that
+leave the fp32 range, query rows that see nothing, light weights beside heavy ones, lengths past the table."""
+import math
+
+import pytest
+import torch
+
+import exact_io_aware_76_b200 as fa
+from test_gpu_cache import DT, E4M3, check, gen, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H,Hkv,Sq,D,dtype", [(16, 8, 1, 128, "bf16"), (16, 8, 1, 64, "f16"), (16, 4, 3, 128, "f16"),
+                                              (16, 2, 4, 64, "bf16")])
+def test_short_units_whose_rows_differ_by_large_factors(H, Hkv, Sq, D, dtype):
+    """Many units of one to three tiles per CTA, the query rows of neighbouring units 2^12 apart: a row factor of the
+    wrong unit changes every score of a row. Equal bits in every run."""
+    g = gen(86)
+    B = 200
+    lens = torch.randint(1, 385, (B,), generator=g, device="cuda").tolist()
+    c = make_cache(lens, Hkv, D, 64, g)
+    q = torch.randn((B, Sq, Hkv, H // Hkv, D), generator=g, device="cuda")
+    unit = torch.arange(B * Hkv, device="cuda").view(B, 1, Hkv, 1, 1)
+    q = (q * torch.where(unit % 2 == 0, 2.0 ** -8, 2.0 ** 4)).view(B, Sq, H, D).to(DT[dtype])
+    out, lse = fa.fwd_cache(q, **c)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 0
+    check(q, c, out, lse, -1, 0, only=range(0, B, 8))
+    for _ in range(20):
+        again = fa.fwd_cache(q, **c)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
