@@ -619,19 +619,20 @@ __device__ __forceinline__ void cache_cleaner(const CacheParams& p, const CacheR
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) << 23); }
 
 // Row scaling of q: with amax the row's largest magnitude, q * mul has its largest element in [128, 256), and a
-// product with it is multiplied by back = 1 / mul. A row with an infinity or a NaN gets back = NaN, so that its scores are
-// NaN as they would be.
-__device__ __forceinline__ void q_row_scale(uint32_t amax_bits, float& mul, float& back) {
+// product with it is multiplied by back = 1 / mul. Returns whether the row is finite. One with an infinity or a NaN is
+// to be NaN where it sees a key, and 0 (LSE -inf) as any other row where it sees none: its callers compute with a row of
+// zeros in its place and turn the row's sum of weights into a NaN at the end, if it has seen a key.
+__device__ __forceinline__ bool q_row_scale(uint32_t amax_bits, float& mul, float& back) {
   // (magnitudes of floats order as their bits; bits of 2^128 and above are infinities and NaNs)
+  const bool finite = amax_bits < 0x7f800000u;
+  if (!finite) amax_bits = 0;
   int e = static_cast<int>(amax_bits >> 23) - 127;
   e = max(e, -100);  // smaller rows keep a fixed factor (0 rows included)
   mul = pow2i(min(7 - e, 127));
   back = pow2i(max(e - 7, -126));
-  if (amax_bits >= 0x7f800000u) {
-    mul = 1.f;
-    back = __int_as_float(0x7fc00000);
-  }
+  return finite;
 }
+constexpr uint32_t kNanBits = 0x7fc00000u;
 
 // Two fp16 numbers -> kParts pairs of 8-bit codes, largest part first. Part q is multiplied by 2^(4 (q % kStack)), so
 // that the parts that lie in different rows of an operand (kStack of them) all use the whole e4m3 range; a part behind
@@ -900,7 +901,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int s = 1; s < kThreadsPerRow; s <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, s));
         float mul, back;
-        q_row_scale(amax, mul, back);
+        if (!q_row_scale(amax, mul, back)) {
+          back = __uint_as_float(kNanBits);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
         if (row_q < R) {
           if (piece == 0) row_back[(unit & 1) * 32 + row_q] = back * p.scale_log2;
 #pragma unroll
@@ -932,7 +937,9 @@ __global__ void __launch_bounds__(384, 1)
         const CacheItem t = walk.item;
         const int hk = walk.at.hk, w0 = walk.at.w;
         const int left = min(run.count - g, t.n - w0);
-        const float c_row = row_back[(unit & 1) * 32 + r];
+        const float factor = row_back[(unit & 1) * 32 + r];
+        const bool finite = factor == factor;  // else see q_row_scale
+        const float c_row = finite ? factor : 0.f;
         const int row = t.row0 + min(r, t.rows - 1);
         const int aligned = t.c0 + row / p.group;
         const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
@@ -1082,7 +1089,7 @@ __global__ void __launch_bounds__(384, 1)
         g += left;
         // ---- the unit's (or piece's) end. The next unit's q first: its scores can run during the join.
         q_m[warp * 32 + lane] = m;
-        q_l[warp * 32 + lane] = l;
+        q_l[warp * 32 + lane] = finite || m == -INFINITY ? l : __uint_as_float(kNanBits);
         const bool whole = left == t.n;
         if (more) {
           // (the last tile's scores may be the other warpgroup's)
@@ -1419,6 +1426,7 @@ __global__ void __launch_bounds__(384, 1)
       // ---- q: this thread's row into the A operand (its previous unit's products are complete: the warpgroup has
       // seen their results)
       float c_row;
+      bool finite;
       {
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(p.q) + ((static_cast<size_t>(item.b) * p.Sq + qi) * p.H + h) * D);
@@ -1426,14 +1434,14 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) amax = q_amax8<kBF16>(src[i], amax);
         float mul, back;
-        q_row_scale(amax, mul, back);
+        finite = q_row_scale(amax, mul, back);
         c_row = back * fabsf(p.scale_log2);  // the scale's sign goes to q, so that larger scores mean larger weights
         c_row = c_row < 1e-37f ? 1e-37f : c_row;  // (never 0: a masked score is -inf)
         mul = copysignf(mul, p.scale_log2);
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           uint2 part[kQParts];
-          q_split8<kBF16, kQParts, 1>(src[i], mul, part);
+          q_split8<kBF16, kQParts, 1>(finite ? src[i] : make_uint4(0u, 0u, 0u, 0u), mul, part);
           uint8_t* dst = smem + L::kQOff + t * L::kRaw + r_tile * 128 + ((i >> 1) ^ (r_tile & 7)) * 16 + (i & 1) * 8;
 #pragma unroll
           for (int q = 0; q < kQParts; ++q) *reinterpret_cast<uint2*>(dst + q * 2 * L::kRaw) = part[q];
@@ -1533,6 +1541,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!mbar_wait(&o_full[t], (step - 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after_sync();
       const bool whole = left == item.n;
+      if (!finite && m != -INFINITY) l = __uint_as_float(kNanBits);  // (see q_row_scale)
       const float inv = l == 0.f ? 0.f : whole ? 1.f / l : 1.f;
       const size_t slot = static_cast<size_t>(cache_slot(blockIdx.x, w0)) * kRows + r;
       uint16_t* orow = static_cast<uint16_t*>(p.out) + ((static_cast<size_t>(item.b) * p.Sq + qi) * p.H + h) * D;

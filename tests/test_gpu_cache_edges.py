@@ -30,3 +30,34 @@ def test_short_units_whose_rows_differ_by_large_factors(H, Hkv, Sq, D, dtype):
     for _ in range(20):
         again = fa.fwd_cache(q, **c)
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("Sq,H,Hkv", [(4, 2, 1), (4, 4, 1), (4, 8, 1), (90, 2, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_query_rows_that_are_not_finite(Sq, H, Hkv, dtype, bad):
+    """A padded batch with NaNs or infinities in its padding: a row that sees no key (shorter sequence, no page) is 0 and
+    -inf whatever its q holds; one that sees a key is NaN; the other rows have the bits that they have beside rows of
+    zeros. One sequence is long enough to be cut between CTAs."""
+    g = gen(87)
+    lens = [3, 0, 20000, 700, 150]
+    c = make_cache(lens, Hkv, 128, 32, g)
+    c["table"][4] = -1
+    q = torch.randn((len(lens), Sq, H, 128), generator=g, device="cuda").to(DT[dtype])
+    rows = torch.zeros((len(lens), Sq, H), dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        rows[b, :max(0, Sq - n), 0] = True  # the padding of one head
+    rows[4, :, 1] = True                    # no pages
+    rows[2, 1, 1] = rows[3, Sq - 1, 0] = True
+    q[rows] = 0
+    want = fa.fwd_cache(q, **c)
+    q[rows] = bad
+    blind = torch.isneginf(want[1]).transpose(1, 2)
+    out, lse = fa.fwd_cache(q, **c)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 0
+    lse, clean = lse.transpose(1, 2), want[1].transpose(1, 2)
+    assert blind[0, :Sq - 3].all() and blind[1].all() and blind[4].all() and not blind[2:4].any()
+    assert not out[blind].any() and torch.isneginf(lse[blind]).all()
+    assert torch.isnan(out[rows & ~blind]).all() and torch.isnan(lse[rows & ~blind]).all()
+    assert torch.equal(out[~rows], want[0][~rows]) and torch.equal(lse[~rows], clean[~rows])
