@@ -1436,7 +1436,6 @@ __global__ void __launch_bounds__(384, 1)
         float mul, back;
         finite = q_row_scale(amax, mul, back);
         c_row = back * fabsf(p.scale_log2);  // the scale's sign goes to q, so that larger scores mean larger weights
-        c_row = c_row < 1e-37f ? 1e-37f : c_row;  // (never 0: a masked score is -inf)
         mul = copysignf(mul, p.scale_log2);
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
@@ -1449,6 +1448,9 @@ __global__ void __launch_bounds__(384, 1)
         fence_proxy_async_smem();
         mbar_arrive(&q_ready[t]);
       }
+      // The factor of a group's scores. Never 0, because a masked score is -inf: a row of zeros (back = 2^-107) over a page of
+      // zeros (scale 2^-50) would underflow. Scores are below 2^25, so at the smallest normal number they count as 0.
+      auto factor = [&](float ks) { return fmaxf(c_row * ks, 1.17549435e-38f); };
       const int aligned = item.c0 + qi;
       const int from = p.win_left >= 0 ? aligned - p.win_left : 0;
       float m = -INFINITY, l = 0.f;
@@ -1478,7 +1480,7 @@ __global__ void __launch_bounds__(384, 1)
             g1 = fmax3(g1, x[16 * gr + c + 2], x[16 * gr + c + 3]);
           }
           g0 = fmax3(g0, g1, fmaxf(x[16 * gr + 14], x[16 * gr + 15]));
-          m_new = fmaxf(m_new, fmaf(g0, c_row * f[gr], f[8 + gr]));
+          m_new = fmaxf(m_new, fmaf(g0, factor(f[gr]), f[8 + gr]));
         }
         if (__any_sync(0xffffffffu, m_new > m + kManyLag)) {
           const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
@@ -1501,7 +1503,7 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t pk[64];
 #pragma unroll
         for (int gr = 0; gr < 8; ++gr) {
-          const float a = c_row * f[gr], b = f[8 + gr] + off;
+          const float a = factor(f[gr]), b = f[8 + gr] + off;
           const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
           uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll

@@ -61,3 +61,27 @@ def test_query_rows_that_are_not_finite(Sq, H, Hkv, dtype, bad):
     assert not out[blind].any() and torch.isneginf(lse[blind]).all()
     assert torch.isnan(out[rows & ~blind]).all() and torch.isnan(lse[rows & ~blind]).all()
     assert torch.equal(out[~rows], want[0][~rows]) and torch.equal(lse[~rows], clean[~rows])
+
+
+@pytest.mark.parametrize("Sq,H", [(4, 2), (4, 4), (8, 4), (90, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [None, 1e-38, -1e-38])
+def test_zeros_in_queries_and_keys(Sq, H, dtype, scale):
+    """A row of zeros over pages of zeros, as an append leaves them (scale 2^-50): the product of the two smallest factors
+    is not to turn masked scores into NaNs. Every visible key counts the same."""
+    n, D, page = 200, 64, 32
+    g = gen(88)
+    m = -(-n // page)
+    c = {x: torch.zeros((m, 1, page, D), device="cuda").to(E4M3) for x in ("k_pages", "v_pages")}
+    c.update({x: torch.ones((m, 1), device="cuda") for x in ("k_scale", "v_scale")})
+    c["table"] = torch.arange(m, device="cuda", dtype=torch.int32)[None].contiguous()
+    c["lens"] = torch.tensor([n], dtype=torch.int32, device="cuda")
+    k = torch.zeros((1, n, 1, D), device="cuda", dtype=DT[dtype])
+    fa.cache_append(k, torch.randn(k.shape, generator=g, device="cuda").to(k.dtype), **c)
+    assert (c["k_scale"] == 2.0 ** -50).all()
+    q = torch.randn((1, Sq, H, D), generator=g, device="cuda").to(DT[dtype])
+    q[:, :, 0] = 0
+    out, lse = fa.fwd_cache(q, **c, scale=scale)
+    check(q, c, out, lse, -1, 0, scale)
+    seen = torch.arange(n - Sq + 1, n + 1, device="cuda").double()
+    assert (lse[0, 0].double() - seen.log()).abs().max() <= 1e-5
