@@ -11,17 +11,18 @@
 // a third part for the 3 bits left is exact as long as the parts stay in range (split_f16x2).
 // Each query row is first scaled by a power of two that brings its largest element to [128, 256); elements below
 // 2^-9 of the largest lose what falls under the last part's smallest step, an absolute error of at most 2^-17 (bf16) or
-// 2^-24 (fp16) of the row's largest element. S = q K^T is the sum of the parts' products in the fp32 accumulator.
-// The probabilities are split the same way (bf16 outputs: relative error 2^-8, as bf16 probabilities have; fp16:
-// 2^-11, set by their fp16 rounding before the split).
+// 2^-21 (fp16) of the row's largest element. S = q K^T is the sum of the parts' products in the fp32 accumulator.
+// The weights are rounded to fp16 (relative error 2^-11) and split exactly into three parts, in e5m2: two significant bits
+// less than e4m3 each and the same 11 in all (every residual is signed, which counts for a bit), but a range down to 2^-16
+// that keeps the light weights beside a heavy one (split_weight).
 //
 // Scales. With ks, vs the scales of key j's page and c = scale * log2 e, the weight that reaches the PV product is
-//   w_ij = 2^(s_ij c ks + log2 vs - m_i + 6),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
+//   w_ij = 2^(s_ij c ks + log2 vs - m_i + 13),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
 // with m_i the running maximum of s c ks + log2 vs: the V scale is part of the exponent, so pages of any scales share one
-// accumulator, and the largest weights have full precision whatever the scales are. The factor 2^6 uses e4m3's
-// range upwards (m may lag by up to 2, so w <= 2^8); what small weights lose lies below 2^-20 of the largest (the
-// smallest half step of the last part, see split_f16x2), about 14 in the exponent of e.
-// Scales lie in [2^-50, 2^50], so l (at most 2^(6+2+100) times the number of keys) stays finite.
+// accumulator, and the largest weights have full precision whatever the scales are. The factor 2^13 uses e5m2's and
+// fp16's range upwards (m may lag by up to 2, so w <= 2^15); what a small weight loses is at most 2^-17, so 2^-30 of the
+// row's largest weight (split_weight), about 20 in the exponent of e below it.
+// Scales lie in [2^-50, 2^50], so l (at most 2^(13+2+50) times the number of keys) stays finite.
 //
 // Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
 // tiles, and before them the tiles with sinks). All units' tiles are laid end to end, each unit's with a few places
@@ -38,7 +39,7 @@ constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that 
 // Beginning and ending a unit takes a CTA about as long as this many tiles.
 constexpr int kCacheUnitCost = 3;
 constexpr float kCacheLag = 2.0f;    // how far the running maximum may lag (log2)
-constexpr float kCacheShift = 6.0f;  // weights carry 2^6 (see above)
+constexpr float kCacheShift = 13.0f;  // weights carry 2^13 (see above)
 // The same for blocks of many rows, whose weights are fp16 (w <= 2^15; what is lost lies below 2^-34 of the largest).
 constexpr float kManyLag = 6.0f, kManyShift = 9.0f;
 
@@ -98,7 +99,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Parts beyond the stacked ones: the third part of fp16 where it has no rows of its own.
+// Parts of q beyond the stacked ones: the third part of fp16 where it has no rows of its own.
 __host__ __device__ constexpr bool part_is_e5m2(int q, int stack) { return q == 2 && stack < 3; }
 template <bool kBF16>
 __device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
@@ -457,11 +458,16 @@ constexpr uint32_t kE5M2A = 1u << 7;  // instruction descriptor, kind::f8f6f4: A
 // Few query rows per unit: R = 8, 16 or 32.
 template <int D, bool kBF16, int R>
 struct CacheSmem {
-  // Parts of q and of the weights. The A operand holds every row 128 / R times, kStack of them with different parts.
-  // Where the parts are not stacked (and so not scaled) the weights get a third one for the sake of small weights.
-  static constexpr int kStack = R == 8 ? (kBF16 ? 2 : 4) : R == 16 ? 2 : 1;
-  static constexpr int kQParts = kBF16 ? 2 : 3, kPParts = kBF16 && kStack > 1 ? 2 : 3;
-  static constexpr int kQPass = (kQParts + kStack - 1) / kStack;  // products per S
+  // Parts of q and of the weights. The A operand holds every row 128 / R times: the lanes of a warp hold it kStack times,
+  // with different parts. Two e4m3 parts of the weights are enough for bf16's 8 bits but drop a weight 2^-20 below the row's
+  // largest; three cost, in a loop, 431 -> 439 us (R = 8, 32 x 32768 tokens, 8 heads of 128), 313 -> 323 us (heads of 64)
+  // and 123 -> 146 us (R = 16, 32 x 16384 tokens, 4 heads of 128: two products per O instead of one).
+  // bf16's two parts of q do not fill four rows: they lie there twice, kQStack rows each time, and the second pair of lanes
+  // takes the second half of the keys, which saves half the exchange of partial scores (448 -> 439 us, as above).
+  static constexpr int kStack = 32 / R;
+  static constexpr int kQParts = kBF16 ? 2 : 3, kPParts = 3;
+  static constexpr int kQStack = kStack < kQParts || !kBF16 ? kStack : 2;
+  static constexpr int kQPass = (kQParts + kQStack - 1) / kQStack;  // products per S
   static constexpr int kPPass = (kPParts + kStack - 1) / kStack;  // products per O
   static constexpr int kTile = 16384;                // 128 rows of one 128-byte swizzle row (head dim 64: half zeros)
   static constexpr int kStages = kQPass == 1 ? 5 : 4;
@@ -683,14 +689,30 @@ __device__ __forceinline__ uint32_t q_amax8(const uint4& v, uint32_t amax) {
   return amax;
 }
 
-// Four weights -> their parts' codes, packed four to a register (first weight lowest).
-template <int kParts, int kStack>
-__device__ __forceinline__ void p_split4(float a, float b, float c, float d, uint32_t* part) {
-  uint32_t lo[kParts], hi[kParts];
-  split_f16x2<kParts, kStack>(pack2_f16(a, b), lo);
-  split_f16x2<kParts, kStack>(pack2_f16(c, d), hi);
+// Two weights, rounded to fp16 (at most 2^15) -> three pairs of e5m2 codes, largest part first, part q multiplied by
+// 2^(4 (q % kStack)) as in split_f16x2. Exact for kStack = 4, and for weights of 2^-6 and above otherwise; what smaller ones
+// lose there is at most 2^-17.
+template <int kStack>
+__device__ __forceinline__ void split_weight(uint32_t h, uint32_t* code) {
 #pragma unroll
-  for (int q = 0; q < kParts; ++q) part[q] = lo[q] | (hi[q] << 16);
+  for (int q = 0; q < 3; ++q) {
+    constexpr uint32_t kUp[3] = {0x3c003c00u, 0x4c004c00u, 0x5c005c00u};    // 1, 2^4, 2^8
+    constexpr uint32_t kDown[3] = {0x3c003c00u, 0x2c002c00u, 0x1c001c00u};  // 1, 2^-4, 2^-8
+    code[q] = e5m2x2_from_f16x2(q % kStack ? mul_f16x2(h, kUp[q % kStack]) : h);
+    if (q < 2) {
+      const uint32_t back = __byte_perm(code[q], 0u, 0x1404);  // e5m2 is the upper byte of fp16
+      h = sub_f16x2(h, q % kStack ? mul_f16x2(back, kDown[q % kStack]) : back);
+    }
+  }
+}
+// Four weights -> their parts' codes, packed four to a register (first weight lowest).
+template <int kStack>
+__device__ __forceinline__ void p_split4(float a, float b, float c, float d, uint32_t* part) {
+  uint32_t lo[3], hi[3];
+  split_weight<kStack>(pack2_f16(a, b), lo);
+  split_weight<kStack>(pack2_f16(c, d), hi);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) part[q] = lo[q] | (hi[q] << 16);
 }
 
 // -------------------------------------------------------------------------------- attention of few query rows
@@ -698,9 +720,8 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 // bytes of the cache bound it, so everything else is arranged to hide behind the copies. An M = 128 product costs the
 // same however few of its rows are used, so the rows are put into the A operand 128 / R times. kStack neighbouring
 // copies hold the parts of q (and later of the weights), so that one product does the work of all parts: their partial
-// scores are added across lanes, and their rows of O at the end. The other copies share out the tile's 128 keys: each
-// warp has 32, and where copies are left its lanes take 16 each; a copy has a running maximum, sum and rows of O of its
-// own, and weights of 0 for the others' keys. Nothing else is exchanged until the copies are joined, once, at the end of
+// scores are added across lanes, and their rows of O at the end. The warps share out the tile's 128 keys, 32 each: a
+// warp's copies have a running maximum, sums and rows of O of their own, and weights of 0 for the other warps' keys. Nothing else is exchanged until the copies are joined, once, at the end of
 // the unit. Measured at 32 x 32768 tokens, 64 query heads on 8, bf16 (2.15 GB: 328 us at the copy rate): one product
 // per part 505 us; one product with all parts 427; two softmax warpgroups 398; each score computed by one lane 383; two
 // warps copying 388, but 526 -> 420 with pages of 16; the issuing warp uniform 371 (91% of the copy rate; 429 in a loop
@@ -718,10 +739,9 @@ __global__ void __launch_bounds__(384, 1)
     fa_cache_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const CacheParams p) {
   using L = CacheSmem<D, kBF16, R>;
-  constexpr int kStages = L::kStages, kStack = L::kStack, kQParts = L::kQParts, kPParts = L::kPParts;
+  constexpr int kStages = L::kStages, kStack = L::kStack, kQStack = L::kQStack, kQParts = L::kQParts, kPParts = L::kPParts;
   constexpr int kQPass = L::kQPass, kPPass = L::kPPass;
   constexpr int kCopies = 8 * (32 / R);  // of a row, in both warpgroups
-  constexpr int kKeys = R * kStack;      // keys whose weights a lane's row of P holds; the lane computes R of them
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -786,7 +806,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 9) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_e4m3(128, 128, false, false);  // (| kE5M2A for the third parts)
-      constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true);
+      constexpr uint32_t id_o = idesc_e4m3(128, 128, false, true) | kE5M2A;
       const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kVOff), 16384, 1024);
@@ -805,7 +825,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             umma_ss_f8_if(lead, d, sdesc_add(q_desc, q * L::kTile + kk * 32), sdesc_add(b0, kk * 32),
-                          id_s | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
+                          id_s | (part_is_e5m2(q * kQStack, kQStack) ? kE5M2A : 0u), (q > 0 || kk > 0) ? 1u : 0u);
         umma_commit_if(lead, &s_full[buf]);
       };
       CacheWalk<R> walk;
@@ -842,8 +862,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int q = 0; q < kPPass; ++q)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts_f8_if(lead, d, a + q * 32 + kk * 8, sdesc_add(b0, kk * 4096),
-                            id_o | (part_is_e5m2(q * kStack, kStack) ? kE5M2A : 0u),
+              umma_ts_f8_if(lead, d, a + q * 32 + kk * 8, sdesc_add(b0, kk * 4096), id_o,
                             (it > 1 || q > 0 || kk > 0) ? 1u : 0u);
           umma_commit_if(lead, &kv_empty[s]);
           s = s1;
@@ -865,9 +884,8 @@ __global__ void __launch_bounds__(384, 1)
       const int wg = warp / 4, quarter = warp % 4;  // even or odd tiles; keys 32 * quarter .. + 31 of a tile
       const uint32_t lane_base = tmem + ((quarter * 32) << 16);
       const uint32_t s_tmem = lane_base + wg * 128, o_tmem = lane_base + 256 + wg * 128;
-      // row; part (and which R of the row's kKeys keys this lane computes); which kKeys of the warp's 32 keys
-      const int r = lane % R, stack = lane / R % kStack, share = lane / kKeys;
-      const float down = pow2i(-4 * stack);
+      const int r = lane % R, stack = lane / R;  // row; part, and which R of the warp's 32 keys this lane computes
+      const float down = pow2i(-4 * stack), down_q = pow2i(-4 * (stack % kQStack));
       int joins = 0;
       auto join = [&]() {  // all threads of these warps, bounded like every wait
         mbar_arrive(joint);
@@ -910,10 +928,10 @@ __global__ void __launch_bounds__(384, 1)
           if (piece == 0) row_back[(unit & 1) * 32 + row_q] = back * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
-            uint2 part[kQPass * kStack];
-            q_split8<kBF16, kQParts, kStack>(v[i], mul, part);
+            uint2 part[kQPass * kQStack];
+            q_split8<kBF16, kQParts, kQStack>(v[i], mul, part);
 #pragma unroll
-            for (int q = kQParts; q < kQPass * kStack; ++q) part[q] = make_uint2(0u, 0u);
+            for (int q = kQParts; q < kQPass * kQStack; ++q) part[q] = make_uint2(0u, 0u);
             const int e8 = piece * kVec + i;  // 8-byte unit of the row
 #pragma unroll
             for (int c = 0; c < 128 / R; ++c) {
@@ -921,7 +939,7 @@ __global__ void __launch_bounds__(384, 1)
               uint8_t* dst = smem + L::kQOff + m * 128 + ((e8 >> 1) ^ (m & 7)) * 16 + (e8 & 1) * 8;
 #pragma unroll
               for (int q = 0; q < kQPass; ++q)
-                *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q * kStack + c % kStack];
+                *reinterpret_cast<uint2*>(dst + q * L::kTile) = part[q * kQStack + c % kQStack];
             }
           }
         }
@@ -952,26 +970,26 @@ __global__ void __launch_bounds__(384, 1)
         const int first = (wg - g) & 1;  // this warpgroup's first tile of the unit
         for (int it = first; it < left; it += 2) {
           const int gi = g + it, s = gi % kStages;
-          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * quarter + kKeys * share + R * stack;
+          const int tile0 = cache_key0(t, w0 + it), key0 = tile0 + 32 * quarter + R * stack;
           if (!mbar_wait(&s_full[wg], (gi >> 1) & 1, abort_flag) ||
               !mbar_wait(&k_full[s], (gi / kStages) & 1, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
-          // Scores of this lane's R keys: the parts' partial scores of all kKeys keys lie in the kStack lanes of the row,
-          // which exchange halves until each has the sums of its own keys.
+          // Scores of this lane's R keys: the parts' partial scores of the R * kQStack keys that contain them lie in
+          // kQStack lanes of the row, which exchange halves until each has the sums of its own keys.
           float x[R];
           {
             float v[32];
             tmem_ld_x32(s_tmem + 32 * quarter, reinterpret_cast<uint32_t*>(v));
-            if (kKeys == 16) {
+            if (kQStack < kStack) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) v[c] = share ? v[16 + c] : v[c];
+              for (int c = 0; c < 16; ++c) v[c] = stack & 2 ? v[16 + c] : v[c];
             }
-            if (kStack > 1) {
+            if (kQStack > 1) {
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c) v[c] *= down;
+              for (int c = 0; c < R * kQStack; ++c) v[c] *= down_q;
             }
 #pragma unroll
-            for (int n = kStack / 2; n > 0; n /= 2) {
+            for (int n = kQStack / 2; n > 0; n /= 2) {
               const bool upper = (stack & n) != 0;
 #pragma unroll
               for (int c = 0; c < R * n; ++c) {
@@ -983,7 +1001,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int c = 0; c < R; ++c) x[c] = v[c];
           }
           // this lane's 16-key groups: one (R <= 16) or two
-          const float* f = fac + s * 24 + 2 * quarter + (kKeys * share + R * stack) / 16;
+          const float* f = fac + s * 24 + 2 * quarter + R * stack / 16;
           const float a0 = c_row * f[0], lv0 = f[8], iv0 = f[16];
           const float a1 = R == 32 ? c_row * f[1] : a0, lv1 = R == 32 ? f[9] : lv0, iv1 = R == 32 ? f[17] : iv0;
 #pragma unroll
@@ -1024,12 +1042,12 @@ __global__ void __launch_bounds__(384, 1)
             for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[c + e] + off);
             (c < 16 ? sum0 : sum1) += (w[0] + w[1]) + (w[2] + w[3]);
             uint32_t code[kPParts];
-            p_split4<kPParts, kStack>(w[0], w[1], w[2], w[3], code);
+            p_split4<kStack>(w[0], w[1], w[2], w[3], code);
 #pragma unroll
             for (int q = 0; q < kPPass * kStack; ++q) part[q][c / 4] = q < kPParts ? code[q] : 0u;
           }
-          // The row of P in product q holds part q * kStack + stack of all kKeys keys: the same lanes exchange parts.
-          uint32_t pk[kPPass][8];  // this warp's 32 keys: zeros but for the lane's kKeys
+          // The row of P in product q holds part q * kStack + stack of the warp's 32 keys: the same lanes exchange parts.
+          uint32_t pk[kPPass][8];
 #pragma unroll
           for (int q = 0; q < kPPass; ++q) {
             uint32_t row_p[kStack][R / 4];
@@ -1064,10 +1082,7 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t own = row_p[k * 4 / R % kStack][k % (R / 4)];
-              pk[q][k] = (kKeys == 32 || k / 4 == share) ? own : 0u;
-            }
+            for (int k = 0; k < 8; ++k) pk[q][k] = row_p[k * 4 / R][k % (R / 4)];
           }
           l += sum0 * iv0 + sum1 * iv1;
           const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};

@@ -257,8 +257,9 @@ FA_API size_t fa_cache_workspace_size(int B, int Sq, int H, int Hkv, int D);
  *   - Scales must lie in 2^-50 .. 2^50 (any fp32 value there, a power of two or not).
  *   - What stands in slots behind a sequence's end, or in tokens that none of the call's queries sees, does not matter (NaNs
  *     included). A non-finite V that some query of the call sees may reach the call's other rows of that K/V head.
- *   - Probabilities reach the PV product with the precision of the output type (relative error 2^-8 or 2^-11); q as it
- *     is, but for elements below 2^-9 of their row's largest (absolute error 2^-17 of that).
+ *   - A key's weight (its probability times its page's V scale) reaches the PV product with a relative error of at most
+ *     2^-11, or an absolute one of 2^-30 of the row's largest weight where that is more; q as it is, but for elements below
+ *     2^-9 of their row's largest (absolute error 2^-17 of that).
  *   - workspace: fa_cache_workspace_size bytes, 256-byte aligned; contents on entry do not matter. Calls that may run
  *     at the same time (two streams, two captured graphs) need a workspace each. Results repeat bit for bit.
  */
