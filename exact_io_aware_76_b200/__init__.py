@@ -17,7 +17,8 @@ right after its aligned key (-1 = unbounded side); the first ``sinks`` keys stay
 
 Every operand (inputs and caller-passed outputs alike) is checked against these shapes, dtypes and the
 device of ``q`` before anything is launched; a mismatch raises ``ValueError`` or ``TypeError``. Each call
-runs with ``q``'s device current and, unless a stream is given, on that device's current stream.
+runs with ``q``'s device current and, unless a stream is given, on that device's current stream. What a call makes
+itself comes from the memory of the stream it runs on, and may be freed on the current stream at any time.
 """
 import contextlib
 import ctypes
@@ -201,11 +202,19 @@ def check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
     return num_pages, page, table.shape[1]
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here (on the current stream) whose memory a call on another stream still uses after it returns."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _new(like, shape, dtype, stream, returned=True):
+    """An uninitialised tensor on ``like``'s device, which is the current one. With a stream given it comes from that
+    stream's memory: what the current stream gave back its own earlier work may still be using. The current stream is
+    recorded for a tensor that is returned, because that is where the caller goes on with it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 def _stream(stream, dev):
@@ -239,24 +248,21 @@ def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, wind
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
     check_sinks(sinks, dropout_p)
     with _device(dev):
-        made = []
+        ptr = _stream(stream, dev)
         if out is None:
-            out = torch.empty_like(q)
-            made.append(out)
+            out = _new(q, q.shape, q.dtype, stream)
         if lse is None:
-            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
-            made.append(lse)
+            lse = _new(q, (B, H, Sq), torch.float32, stream)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         shape = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
                  int(bool(causal)), _bound(window[0]), _bound(window[1]))
         sc = (float(0.0 if scale is None else scale), _dtype_code(q))
         if dropout_p:
-            rc = lib().fa_fwd_dropout(*shape, *sc, float(dropout_p), int(seed), int(offset), _stream(stream, dev))
+            rc = lib().fa_fwd_dropout(*shape, *sc, float(dropout_p), int(seed), int(offset), ptr)
         elif sinks:
-            rc = lib().fa_fwd_sink(*shape, int(sinks), *sc, _stream(stream, dev))
+            rc = lib().fa_fwd_sink(*shape, int(sinks), *sc, ptr)
         else:
-            rc = lib().fa_fwd_ex(*shape, *sc, _stream(stream, dev))
-        _used_on(stream, *made)
+            rc = lib().fa_fwd_ex(*shape, *sc, ptr)
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_dropout" if dropout_p else "fa_fwd_sink" if sinks else "fa_fwd_ex")
     return out, lse
@@ -270,15 +276,16 @@ def fwd_fp8(q, k, v, causal=False, scale=None, descale=(1.0, 1.0, 1.0), out=None
 
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float8_e4m3fn,))
     with _device(dev):
+        ptr = _stream(stream, dev)
         if out is None:
-            out = torch.empty((B, Sq, H, D), dtype=torch.bfloat16, device=dev)
+            out = _new(q, (B, Sq, H, D), torch.bfloat16, stream)
         if lse is None:
-            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
+            lse = _new(q, (B, H, Sq), torch.float32, stream)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, torch.bfloat16)
         rc = lib().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk,
                               H, Hkv, D, int(bool(causal)), _bound(window[0]), _bound(window[1]),
                               float(0.0 if scale is None else scale), float(descale[0]), float(descale[1]),
-                              float(descale[2]), _stream(stream, dev))
+                              float(descale[2]), ptr)
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_fp8")
     return out, lse
@@ -307,23 +314,21 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
     if stage != -1 and (dropout_p or Hkv != H or tuple(window) != (-1, -1) or sinks):
         raise ValueError("single backward stages are available for plain attention only")
     with _device(dev):
-        made = [x for x, given in ((q, dq), (k, dk), (v, dv)) if given is None]
-        made = [torch.empty_like(x) for x in made]
-        fresh = iter(made)
-        dq, dk, dv = (next(fresh) if x is None else x for x in (dq, dk, dv))
+        ptr = _stream(stream, dev)
+        dq, dk, dv = (_new(x, x.shape, x.dtype, stream) if given is None else given
+                      for x, given in ((q, dq), (k, dk), (v, dv)))
         if sinks:
             ws_bytes = sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks)
         else:
             ws_bytes = workspace_size(B, Sq, H, D)
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Sq, H, D, dev)
         if workspace is None:
-            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
-            made.append(workspace)
+            workspace = _new(q, max(ws_bytes, 1), torch.uint8, stream, returned=False)
         sc = float(0.0 if scale is None else scale)
         bounds = (_bound(window[0]), _bound(window[1]))
         ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
-        ws_args = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev))
+        ws_args = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), ptr)
         if dropout_p:
             rc = lib().fa_bwd_dropout(*ptrs, B, Sq, Sk, H, Hkv, D, int(bool(causal)), *bounds, sc,
                                       _dtype_code(q), float(dropout_p), int(seed), int(offset), *ws_args)
@@ -336,7 +341,6 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
         else:
             rc = lib().fa_bwd_stage(int(stage), *ptrs, B, Sq, Sk, H, D, int(bool(causal)), sc, _dtype_code(q),
                                     *ws_args)
-        _used_on(stream, *made)
     if rc != FA_OK:
         raise FAError(rc, "fa_bwd_sink" if sinks else "fa_bwd")
     return dq, dk, dv
@@ -351,14 +355,13 @@ def bwd_noalloc(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=N
     if Hkv != H:
         raise ValueError("the no-alloc backward takes as many K/V heads as query heads")
     with _device(dev):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
+        ptr = _stream(stream, dev)
+        dq, dk, dv = (_new(x, x.shape, x.dtype, stream) if given is None else given
+                      for x, given in ((q, dq), (k, dk), (v, dv)))
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, None, 0, B, Sq, H, D, dev)
         rc = lib().fa_bwd_noalloc(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                   dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Sq, Sk, H, D,
-                                  int(bool(causal)), float(0.0 if scale is None else scale), _dtype_code(q),
-                                  _stream(stream, dev))
+                                  int(bool(causal)), float(0.0 if scale is None else scale), _dtype_code(q), ptr)
     if rc != FA_OK:
         raise FAError(rc, "fa_bwd_noalloc")
     return dq, dk, dv
@@ -417,18 +420,15 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, wi
     num_pages, page, max_pages = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
     check_sinks(sinks, 0.0)
     with _device(dev):
-        made = []
+        ptr = _stream(stream, dev)
         if out is None:
-            out = torch.empty_like(q)
-            made.append(out)
+            out = _new(q, q.shape, q.dtype, stream)
         if lse is None:
-            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
-            made.append(lse)
+            lse = _new(q, (B, H, Sq), torch.float32, stream)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         ws_bytes = cache_workspace_size(B, Sq, H, Hkv, D)
         if workspace is None:
-            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
-            made.append(workspace)
+            workspace = _new(q, max(ws_bytes, 1), torch.uint8, stream, returned=False)
         _check("workspace", workspace, dev)
         if workspace.numel() * workspace.element_size() < ws_bytes:
             raise ValueError("workspace must hold at least %d bytes" % ws_bytes)
@@ -436,8 +436,7 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, wi
                                 v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                 B, Sq, H, Hkv, D, num_pages, page, max_pages, _bound(window_left), int(sinks),
                                 float(0.0 if scale is None else scale), _dtype_code(q), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(stream, dev))
-        _used_on(stream, *made)
+                                workspace.numel() * workspace.element_size(), ptr)
     if rc != FA_OK:
         raise FAError(rc, "fa_cache_fwd")
     return out, lse
