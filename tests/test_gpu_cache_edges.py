@@ -115,3 +115,36 @@ def test_light_weights_beside_a_heavy_one(Sq, H, dtype, heavy):
         off = (out[..., 1].double() / want - 1).abs().max()
         assert off <= tol, (d, float(off), tol)
         assert (lse.double() - (d + torch.log1p(light))).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("Sq,H", [(1, 8), (3, 8), (4, 8), (90, 2)])
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (200, 5)])
+def test_lengths_past_the_table(Sq, H, left, sinks):
+    """A length beyond max_pages * page counts as that many tokens in the attention; an append drops what lies beyond, in a
+    cache whose other pages and slots keep their bytes."""
+    g = gen(89)
+    page, Hkv, D = 32, 1, 64
+    c = make_cache([1504, 1504], Hkv, D, page, g, width=47)  # as many tokens as the table has places for
+    c["lens"][1] = 300
+    q = torch.randn((2, Sq, H, D), generator=g, device="cuda").to(torch.bfloat16)
+    want = fa.fwd_cache(q, **c, window_left=left, sinks=sinks)
+    check(q, c, *want, left, sinks)
+    for n in (1505, 10 ** 6, 2 ** 31 - 1):
+        c["lens"][0] = n
+        got = fa.fwd_cache(q, **c, window_left=left, sinks=sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c["lens"][0], c["lens"][1] = 1510, 0
+    k, v = (torch.randn((2, 10, Hkv, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    before = {x: c[x].clone() for x in ("k_pages", "v_pages", "k_scale", "v_scale")}
+    once = {**c, **{x: t.clone() for x, t in before.items()}, "lens": torch.tensor([1504, 0], dtype=torch.int32, device="cuda")}
+    fa.cache_append(k[:, :4].contiguous(), v[:, :4].contiguous(), **once)  # the four that have a place
+    fa.cache_append(k, v, **c)
+    for x in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        assert torch.equal(c[x].view(torch.uint8), once[x].view(torch.uint8))
+    last = int(c["table"][0, 46])
+    assert not torch.equal(c["k_pages"][last].view(torch.uint8), before["k_pages"][last].view(torch.uint8))
+    for n in (1600, 2 ** 31 - 1):
+        c["lens"][0] = n
+        fa.cache_append(k, v, **c)  # none has a place
+        assert torch.equal(c["k_pages"].view(torch.uint8), once["k_pages"].view(torch.uint8))
+    assert fa.device_status() == 0
