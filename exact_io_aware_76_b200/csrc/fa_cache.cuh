@@ -27,8 +27,7 @@
 // Work split. A unit is (sequence, block of query rows, K/V head); its walk is the 128-key tiles its rows see (window
 // tiles, and before them the tiles with sinks). All units' tiles are laid end to end, each unit's with a few places
 // before them for what a unit costs by itself (kCacheUnitCost), and every CTA takes an equal run of places, whatever the
-// lengths are, so neither one long sequence nor many short ones load the SMs unevenly (32 sequences of 100 to 8000
-// tokens: 110 us with places for tiles only, 73 us with 3 more per unit). Units cut by a run's border leave fp32 partial
+// lengths are, so neither one long sequence nor many short ones load the SMs unevenly. Units cut by a run's border leave fp32 partial
 // sums (O, m, l) in the workspace, and fa_cache_join_kernel adds them in key order, so results repeat bit for bit.
 #pragma once
 #include "fa_fwd.cuh"
@@ -36,7 +35,15 @@
 namespace fa {
 
 constexpr int kCacheCtas = 148;      // one CTA per SM; a fixed number, so that the workspace size needs no device
-// Beginning and ending a unit takes a CTA about as long as this many tiles.
+// Beginning and ending a unit takes a CTA about as long as this many tiles. Measured in a loop with 0 / 1 / 3 / 6 / 12 places
+// per unit (us; bf16, pages of 64):
+//    8 rows, 8 heads of 128, 32 sequences of 100 to 8000 tokens    95 /  88 /  76 /  74 /  76    (heads of 64: 70 / 68 / 61 / 57 / 60)
+//    8 rows, 8 heads of 128, 64 sequences of 100 to 1000           61 /  51 /  43 /  42 /  43    (51 / 45 / 37 / 37 / 39)
+//   16 rows, 4 heads of 128, 100 to 8000                           73 /  65 /  55 /  54 /  59    (52 / 47 / 42 / 44 / 46)
+//   32 rows, 4 heads of 128, 100 to 8000                           82 /  74 /  62 /  61 /  66    (58 / 53 / 52 / 53 / 57)
+//  256 rows, 8 heads of 128, 16 sequences of 300 to 8000          212 / 186 / 173 / 156 / 149    (150 / 137 / 131 / 124 / 129)
+// 3 is within 7% of the best for up to 32 rows. Units of 256 rows would be 4 to 18% faster with 6 (a number of their own is
+// not built).
 constexpr int kCacheUnitCost = 3;
 constexpr float kCacheLag = 2.0f;    // how far the running maximum may lag (log2)
 constexpr float kCacheShift = 13.0f;  // weights carry 2^13 (see above)
@@ -724,9 +731,11 @@ __device__ __forceinline__ void p_split4(float a, float b, float c, float d, uin
 // warp's copies have a running maximum, sums and rows of O of their own, and weights of 0 for the other warps' keys. Nothing else is exchanged until the copies are joined, once, at the end of
 // the unit. Measured at 32 x 32768 tokens, 64 query heads on 8, bf16 (2.15 GB: 328 us at the copy rate): one product
 // per part 505 us; one product with all parts 427; two softmax warpgroups 398; each score computed by one lane 383; two
-// warps copying 388, but 526 -> 420 with pages of 16; the issuing warp uniform 371 (91% of the copy rate; 429 in a loop
-// of seconds, where the power cap holds the SMs at 1.43 GHz and the same copy takes 335). What bounds it then is the chain
-// issue -> scores -> weights -> issue, 1240 cycles a tile as traced (the trace's own stores included).
+// warps copying 388, but 526 -> 420 with pages of 16; the issuing warp uniform 371; a third part of the weights, for the
+// light ones' sake, 389 for single calls (84% of the copy rate; fp16 406) and 448 in a loop of seconds (73%; fp16 463),
+// where the power cap holds the SMs at 1.47 GHz and the same copy takes 331. Heads of 64: 315 and 328 us, half the copy
+// rate. What bounds it is the chain issue -> scores -> weights -> issue, 1300 cycles a tile as traced (1360 in fp16, 1150
+// for heads of 64; the trace's own stores included).
 //
 // Warps: 0-3 and 4-7 softmax of the even and the odd tiles of the run, each warpgroup with its own S and O (so its own
 // maxima and sums too, joined with the others at the end): two tiles are in work at any time, and a warpgroup's

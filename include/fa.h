@@ -239,8 +239,8 @@ FA_API int fa_bwd_noalloc(const void* q, const void* k, const void* v, const voi
  *     where that grows, its codes move to it (exact but for codes that become subnormal). A page's first token
  *     starts a new scale, whatever the page held before.
  *   - Rounding is to nearest even; infinities become +-448 times the scale, NaNs stay NaNs.
- *   - Tokens without a page are dropped. Slots behind the last token are left as they were. No two sequences of a
- *     call may append to the same page.
+ *   - Tokens without a page are dropped. Slots behind the last token are left as they were. A call may append to a page
+ *     in one place only: neither two sequences nor two places of one may have new tokens in the same page.
  */
 FA_API int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale, float* v_scale,
                            const int* table, const int* lens, const int* counts, int B, int T, int Hkv, int D,
