@@ -41,3 +41,28 @@ def test_memory_the_current_stream_still_uses(name):
     torch.cuda.synchronize()
     assert fa.device_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("name", ["fwd", "fwd with sinks", "fwd_fp8", "bwd", "fwd_cache"])
+def test_captured_on_a_side_stream(name):
+    """Two calls on two branches of one captured graph, each with tensors and workspaces of its own; replays agree."""
+    call = calls()[name]
+    want = call()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        for s in side:
+            s.wait_stream(here)
+        got = [call(stream=s) for s in side]
+        for s in side:
+            here.wait_stream(s)
+    for _ in range(3):
+        for r in got:
+            for x in r:
+                x.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+    assert fa.device_status() == 0
