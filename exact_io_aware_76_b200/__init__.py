@@ -202,18 +202,43 @@ def check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
     return num_pages, page, table.shape[1]
 
 
-def _new(like, shape, dtype, stream, returned=True):
-    """An uninitialised tensor on ``like``'s device, which is the current one. With a stream given it comes from that
-    stream's memory: what the current stream gave back its own earlier work may still be using. The current stream is
-    recorded for a tensor that is returned, because that is where the caller goes on with it."""
+_NOTHING = contextlib.nullcontext()
+
+
+class _OnStream:
+    """Makes a stream the current one of its device (which is current)."""
+
+    def __init__(self, stream, caller):
+        import torch
+
+        self.set, self.stream, self.caller = torch.cuda.set_stream, stream, caller
+
+    def __enter__(self):
+        self.set(self.stream)
+
+    def __exit__(self, *exc):
+        self.set(self.caller)
+
+
+def _memory_of(stream, caller):
+    """The context in which a call makes its tensors: they come from the memory of the stream it runs on. (With a stream
+    given, what the current one gave back its own earlier work may still be using.)"""
+    return _NOTHING if stream is None else _OnStream(stream, caller)
+
+
+def _caller(stream, dev):
+    """The current stream where it is not the one that a call runs on: see ``_returned``."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return None
     import torch
 
-    with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(like.device))
+    return torch.cuda.current_stream(dev)
+
+
+def _returned(t, caller):
+    """A tensor that a call made and returns: the caller goes on with it on the current stream, and may free it there."""
+    if caller is not None:
+        t.record_stream(caller)
     return t
 
 
@@ -247,12 +272,12 @@ def fwd(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, wind
 
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
     check_sinks(sinks, dropout_p)
-    with _device(dev):
-        ptr = _stream(stream, dev)
+    ptr, caller = _stream(stream, dev), _caller(stream, dev)
+    with _device(dev), _memory_of(stream, caller):
         if out is None:
-            out = _new(q, q.shape, q.dtype, stream)
+            out = _returned(torch.empty_like(q), caller)
         if lse is None:
-            lse = _new(q, (B, H, Sq), torch.float32, stream)
+            lse = _returned(q.new_empty((B, H, Sq), dtype=torch.float32), caller)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         shape = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk, H, Hkv, D,
                  int(bool(causal)), _bound(window[0]), _bound(window[1]))
@@ -275,12 +300,12 @@ def fwd_fp8(q, k, v, causal=False, scale=None, descale=(1.0, 1.0, 1.0), out=None
     import torch
 
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float8_e4m3fn,))
-    with _device(dev):
-        ptr = _stream(stream, dev)
+    ptr, caller = _stream(stream, dev), _caller(stream, dev)
+    with _device(dev), _memory_of(stream, caller):
         if out is None:
-            out = _new(q, (B, Sq, H, D), torch.bfloat16, stream)
+            out = _returned(q.new_empty((B, Sq, H, D), dtype=torch.bfloat16), caller)
         if lse is None:
-            lse = _new(q, (B, H, Sq), torch.float32, stream)
+            lse = _returned(q.new_empty((B, H, Sq), dtype=torch.float32), caller)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, torch.bfloat16)
         rc = lib().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk,
                               H, Hkv, D, int(bool(causal)), _bound(window[0]), _bound(window[1]),
@@ -313,17 +338,18 @@ def bwd(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=
     check_sinks(sinks, dropout_p)
     if stage != -1 and (dropout_p or Hkv != H or tuple(window) != (-1, -1) or sinks):
         raise ValueError("single backward stages are available for plain attention only")
-    with _device(dev):
-        ptr = _stream(stream, dev)
-        dq, dk, dv = (_new(x, x.shape, x.dtype, stream) if given is None else given
-                      for x, given in ((q, dq), (k, dk), (v, dv)))
+    ptr, caller = _stream(stream, dev), _caller(stream, dev)
+    with _device(dev), _memory_of(stream, caller):
+        dq = _returned(torch.empty_like(q), caller) if dq is None else dq
+        dk = _returned(torch.empty_like(k), caller) if dk is None else dk
+        dv = _returned(torch.empty_like(v), caller) if dv is None else dv
         if sinks:
             ws_bytes = sink_workspace_size(B, Sq, Sk, H, Hkv, D, causal, window, sinks)
         else:
             ws_bytes = workspace_size(B, Sq, H, D)
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, workspace, ws_bytes, B, Sq, H, D, dev)
         if workspace is None:
-            workspace = _new(q, max(ws_bytes, 1), torch.uint8, stream, returned=False)
+            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
         sc = float(0.0 if scale is None else scale)
         bounds = (_bound(window[0]), _bound(window[1]))
         ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
@@ -354,10 +380,11 @@ def bwd_noalloc(q, k, v, out, lse, dout, causal=False, scale=None, dq=None, dk=N
     B, Sq, Sk, H, Hkv, D, dev = check_qkv(q, k, v, (torch.float16, torch.bfloat16))
     if Hkv != H:
         raise ValueError("the no-alloc backward takes as many K/V heads as query heads")
-    with _device(dev):
-        ptr = _stream(stream, dev)
-        dq, dk, dv = (_new(x, x.shape, x.dtype, stream) if given is None else given
-                      for x, given in ((q, dq), (k, dk), (v, dv)))
+    ptr, caller = _stream(stream, dev), _caller(stream, dev)
+    with _device(dev), _memory_of(stream, caller):
+        dq = _returned(torch.empty_like(q), caller) if dq is None else dq
+        dk = _returned(torch.empty_like(k), caller) if dk is None else dk
+        dv = _returned(torch.empty_like(v), caller) if dv is None else dv
         check_bwd_operands(q, k, out, lse, dout, dq, dk, dv, None, 0, B, Sq, H, D, dev)
         rc = lib().fa_bwd_noalloc(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                   dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Sq, Sk, H, D,
@@ -419,16 +446,16 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale=None, wi
         raise ValueError("the K/V head count %d must divide the query head count %d" % (Hkv, H))
     num_pages, page, max_pages = check_cache(k_pages, v_pages, k_scale, v_scale, table, lens, B, Hkv, D, dev)
     check_sinks(sinks, 0.0)
-    with _device(dev):
-        ptr = _stream(stream, dev)
+    ptr, caller = _stream(stream, dev), _caller(stream, dev)
+    with _device(dev), _memory_of(stream, caller):
         if out is None:
-            out = _new(q, q.shape, q.dtype, stream)
+            out = _returned(torch.empty_like(q), caller)
         if lse is None:
-            lse = _new(q, (B, H, Sq), torch.float32, stream)
+            lse = _returned(q.new_empty((B, H, Sq), dtype=torch.float32), caller)
         check_fwd_outputs(out, lse, B, Sq, H, D, dev, q.dtype)
         ws_bytes = cache_workspace_size(B, Sq, H, Hkv, D)
         if workspace is None:
-            workspace = _new(q, max(ws_bytes, 1), torch.uint8, stream, returned=False)
+            workspace = q.new_empty(max(ws_bytes, 1), dtype=torch.uint8)
         _check("workspace", workspace, dev)
         if workspace.numel() * workspace.element_size() < ws_bytes:
             raise ValueError("workspace must hold at least %d bytes" % ws_bytes)

@@ -15,8 +15,8 @@ made = []
 class S(T):
     """A stand-in that notes the stream under which it makes tensors."""
 
-    def new_empty(self, shape, dtype):
-        t = S((shape,) if isinstance(shape, int) else shape, dtype, self.device)
+    def new_empty(self, shape, dtype=None):
+        t = S((shape,) if isinstance(shape, int) else shape, dtype or self.dtype, self.device)
         t.stream, t.recorded = torch.cuda.current_stream(self.device), []
         made.append(t)
         return t
@@ -28,23 +28,17 @@ class S(T):
 @pytest.fixture
 def streams(monkeypatch):
     current = ["current"]
-
-    @contextlib.contextmanager
-    def use(stream):
-        current.append(stream)
-        try:
-            yield
-        finally:
-            current.pop()
-
-    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "set_stream", lambda stream: current.append(stream))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: current[-1])
+    monkeypatch.setattr(torch, "empty_like", lambda x: x.new_empty(x.shape))
     monkeypatch.setattr(fa, "lib", lambda: FakeLib([]))
     monkeypatch.setattr(fa, "_device", lambda dev: contextlib.nullcontext())
     monkeypatch.setattr(fa, "_stream", lambda stream, dev: None)
     for size in ("workspace_size", "sink_workspace_size", "cache_workspace_size"):
         monkeypatch.setattr(fa, size, lambda *a: 1024)
     made.clear()
+    yield
+    assert current[-1] == "current"
 
 
 def qkv(dtype=BF16, Hkv=4):
