@@ -12,9 +12,9 @@
 // Each query row is first scaled by a power of two that brings its largest element to [128, 256); elements below
 // 2^-9 of the largest lose what falls under the last part's smallest step, an absolute error of at most 2^-17 (bf16) or
 // 2^-21 (fp16) of the row's largest element. S = q K^T is the sum of the parts' products in the fp32 accumulator.
-// The weights are rounded to fp16 (relative error 2^-11) and split exactly into three parts, in e5m2: two significant bits
-// less than e4m3 each and the same 11 in all (every residual is signed, which counts for a bit), but a range down to 2^-16
-// that keeps the light weights beside a heavy one (split_weight).
+// The weights are rounded to fp16 (relative error 2^-11) and split exactly into three parts, in e5m2: a significant bit
+// less than e4m3 each, still 11 in all (every residual is signed, which counts for a bit), and a range down to 2^-16 that
+// keeps the light weights beside a heavy one (split_weight).
 //
 // Scales. With ks, vs the scales of key j's page and c = scale * log2 e, the weight that reaches the PV product is
 //   w_ij = 2^(s_ij c ks + log2 vs - m_i + 13),   O_i = sum_j w_ij v_j / l_i,   l_i = sum_j w_ij / vs_j,
